@@ -1,7 +1,8 @@
 """MI355X (gfx950) forward pass of one Mixture-of-Experts FFN layer.
 
-A thin binding over the C ABI of ``libmoe_gfx950.so`` (include/moe.h): each function
-here has the C entry point's name, takes torch tensors that live on the GPU, allocates
+A thin binding over the C ABI of ``libmoe_gfx950.so`` (include/moe.h, and
+include/moe_ops.h for the operators beside the layer forward): each function here
+has the C entry point's name, takes torch tensors that live on the GPU, allocates
 the outputs with torch and passes raw pointers plus the current HIP stream.  Every
 step runs in the library's HIP kernels; nothing is computed in Python.
 """
@@ -28,6 +29,8 @@ __all__ = [
     "grouped_gemm_f32", "moe_combine", "moe_layer_workspace_size", "moe_layer_fwd", "MoeError",
     "moe_layer_chunked_workspace_size", "moe_layer_fwd_chunked",
     "LayerDesc", "moe_probe_mfma_fp8", "moe_probe_hbm_read",
+    "moe_quant_weight_int4_group", "moe_matvec_int4", "moe_ffn_int4", "moe_balance_loss",
+    "moe_route_bwd",
 ]
 
 
@@ -372,6 +375,196 @@ def moe_combine(o: torch.Tensor, row_of_slot: torch.Tensor, topk_w: torch.Tensor
     _lib.check(_lib_().moe_combine(_ptr(o), _dt(o), _ptr(row_of_slot), _ptr(topk_w), T, k, d,
                                    _ptr(y), _dt(y), _stream(dev)), "moe_combine")
     return y
+
+
+# ------------------------------------------- few tokens with 4-bit expert weights
+
+def _want(fn: str, name: str, t: Optional[torch.Tensor], dtype, *shape):
+    """Refuse a tensor of another dtype or shape than the call takes (None passes)."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+        raise ValueError(f"{fn}: {name} must be {dtype} {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)}")
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _int4_weight(fn: str, name: str, q: torch.Tensor, s7: torch.Tensor):
+    """(G, rows, K, group) of int4 codes [G, rows, K/2] and scales [G, rows, K/group]."""
+    if q.dim() != 3 or s7.dim() != 3 or q.dtype != torch.uint8 or s7.dtype != torch.float32 \
+            or q.shape[:2] != s7.shape[:2] or s7.shape[2] == 0 \
+            or (2 * q.shape[2]) % s7.shape[2]:
+        raise ValueError(f"{fn}: {name} must be uint8 codes [G, rows, K/2] with fp32 scales "
+                         f"[G, rows, K/group], got {q.dtype} {list(q.shape)} and {s7.dtype} "
+                         f"{list(s7.shape)}")
+    K = 2 * q.shape[2]
+    return q.shape[0], q.shape[1], K, K // s7.shape[2]
+
+
+@_on_tensor_device
+def moe_quant_weight_int4_group(w: torch.Tensor, group: int):
+    """fp32 weights [G, N, K] -> int4 codes [G, N, K/2] and scales [G, N, K/group], one scale
+    per `group` (32, 64 or 128) weights of a row."""
+    fn = "moe_quant_weight_int4_group"
+    G, N, K = w.shape
+    if w.dtype != torch.float32 or group not in (32, 64, 128) or K % group:
+        raise ValueError(f"{fn}: w must be fp32 with K a multiple of group (32, 64 or 128), got "
+                         f"{w.dtype}, K = {K}, group = {group}")
+    q = torch.empty((G, N, K // 2), dtype=torch.uint8, device=w.device)
+    s7 = torch.empty((G, N, K // group), dtype=torch.float32, device=w.device)
+    _lib.check(_lib_().moe_quant_weight_int4_group(_ptr(w), G, N, K, group, _ptr(q), _ptr(s7),
+                                                   _stream(w.device)), fn)
+    return q, s7
+
+
+@_on_tensor_device
+def moe_matvec_int4(x: torch.Tensor, q: torch.Tensor, s7: torch.Tensor,
+                    idx: Optional[torch.Tensor] = None, x_div: int = 1, swiglu: bool = False,
+                    out_dtype: Optional[torch.dtype] = None):
+    """Products of a few rows x [rows, K] with int4 weights q [G, Nb, K/2], s7 [G, Nb,
+    K/group].  Slot s takes row s // x_div and expert idx[s] (int32 [S]; rows of slots whose
+    expert lies outside [0, G) are zeros); without idx every row takes matrix 0 (x_div 1).
+    Returns y [S, N] of out_dtype (x's by default), N = Nb or, with swiglu, Nb / 2."""
+    fn = "moe_matvec_int4"
+    G, rows, K, group = _int4_weight(fn, "q, s7", q, s7)
+    if swiglu and rows % 2:
+        raise ValueError(f"{fn}: swiglu needs an even number of weight rows, got {rows}")
+    N = rows // 2 if swiglu else rows
+    if x_div < 1:
+        raise ValueError(f"{fn}: x_div must be >= 1")
+    if idx is None:
+        if x_div != 1:
+            raise ValueError(f"{fn}: x_div needs idx")
+        S = x.shape[0]
+    else:
+        S = idx.numel()
+        _want(fn, "idx", idx, torch.int32, S)
+    _want(fn, "x", x, x.dtype, (S + x_div - 1) // x_div, K)
+    x_dt = _dt(x)
+    y = torch.empty((S, N), dtype=out_dtype or x.dtype, device=x.device)
+    _lib.check(_lib_().moe_matvec_int4(_ptr(x), x_dt, x_div, _ptr(q), _ptr(s7), group,
+                                       _ptr(idx), S, G, N, K,
+                                       MOE_EPI_SWIGLU if swiglu else MOE_EPI_PLAIN, _ptr(y),
+                                       _dt(y), _stream(x.device)), fn)
+    return y
+
+
+def moe_ffn_int4_workspace_size(T: int, k: int, d: int, I: int) -> int:
+    return _lib_().moe_ffn_int4_workspace_size(T, k, d, I)
+
+
+@_on_tensor_device
+def moe_ffn_int4(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor,
+                 s2: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                 workspace: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """The routed experts' FFN of a few tokens x [T, d] with int4 weights w13 [E, 2I, d/2]
+    (gate rows, then up rows) and w2 [E, d, I/2], after moe_route: the weighted sum over each
+    token's experts topk_idx [T, k].  Returns y [T, d] of x's dtype."""
+    fn = "moe_ffn_int4"
+    E, rows, d, group = _int4_weight(fn, "w13, s13", w13, s13)
+    I = rows // 2
+    T, k = topk_idx.shape
+    if _int4_weight(fn, "w2, s2", w2, s2) != (E, d, I, group) or rows % 2:
+        raise ValueError(f"{fn}: w13 {list(w13.shape)} and w2 {list(w2.shape)} must be "
+                         "[E, 2I, d/2] and [E, d, I/2] with the same group")
+    _want(fn, "x", x, x.dtype, T, d)
+    _want(fn, "topk_idx", topk_idx, torch.int32, T, k)
+    _want(fn, "topk_w", topk_w, torch.float32, T, k)
+    dt = _dt(x)
+    if y is None:
+        y = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    _want(fn, "y", y, x.dtype, T, d)
+    if workspace is None:
+        workspace = torch.empty(moe_ffn_int4_workspace_size(T, k, d, I), dtype=torch.uint8,
+                                device=x.device)
+    _lib.check(_lib_().moe_ffn_int4(_ptr(x), dt, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
+                                    group, _ptr(topk_idx), _ptr(topk_w), T, k, E, d, I, _ptr(y),
+                                    _ptr(workspace), _nbytes(workspace), _stream(x.device)), fn)
+    return y
+
+
+# --------------------------------------------------- the router's training side
+
+def moe_balance_workspace_size(T: int, E: int, B: int = 1) -> int:
+    return _lib_().moe_balance_workspace_size(T, E, B)
+
+
+def moe_route_bwd_workspace_size(T: int, E: int) -> int:
+    return _lib_().moe_route_bwd_workspace_size(T, E)
+
+
+def _router_args(fn, logits, topk_idx, bias, mask, offsets):
+    T, E = logits.shape
+    B = 1 if offsets is None else offsets.numel() - 1
+    k = topk_idx.shape[1] if topk_idx is not None else 1
+    _want(fn, "logits", logits, torch.float32, T, E)
+    _want(fn, "topk_idx", topk_idx, torch.int32, T, k)
+    _want(fn, "bias", bias, torch.float32, E)
+    _want(fn, "offsets", offsets, torch.int32, B + 1)
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    _want(fn, "mask", mask, torch.uint8, T)
+    return T, E, k, B, mask
+
+
+@_on_tensor_device
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                     offsets: Optional[torch.Tensor] = None, coef: float = 0.01,
+                     kind: str = "switch", workspace: Optional[torch.Tensor] = None):
+    """Load-balance loss of a routed batch (logits [T, E], topk_idx [T, k] of moe_route), over
+    the segments offsets [B+1] (int32; None: the whole batch) and the tokens whose mask byte
+    is nonzero.  kind "switch": coef E sum f_e P_e; "square": coef sum (P_e - 1/E)^2.
+    Returns (loss [], counts [B, E], probs [B, E], grad [B, E]); grad goes to moe_route_bwd."""
+    fn = "moe_balance_loss"
+    kinds = {"switch": _lib.MOE_BALANCE_SWITCH, "square": _lib.MOE_BALANCE_SQUARE}
+    if kind not in kinds:
+        raise ValueError(f"{fn}: kind must be one of {sorted(kinds)}, got {kind!r}")
+    T, E, k, B, mask = _router_args(fn, logits, topk_idx, bias, mask, offsets)
+    dev = logits.device
+    counts = torch.empty((B, E), dtype=torch.int32, device=dev)
+    probs = torch.empty((B, E), dtype=torch.float32, device=dev)
+    grad = torch.empty((B, E), dtype=torch.float32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(moe_balance_workspace_size(T, E, B), dtype=torch.uint8, device=dev)
+    _lib.check(_lib_().moe_balance_loss(_ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(mask),
+                                        _ptr(offsets), T, E, k, B, kinds[kind], coef,
+                                        _ptr(counts), _ptr(probs), _ptr(grad), _ptr(loss),
+                                        _ptr(workspace), _nbytes(workspace), _stream(dev)), fn)
+    return loss, counts, probs, grad
+
+
+@_on_tensor_device
+def moe_route_bwd(logits: torch.Tensor, topk_idx: Optional[torch.Tensor] = None,
+                  dtopk_w: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  renorm: bool = False, mask: Optional[torch.Tensor] = None,
+                  offsets: Optional[torch.Tensor] = None,
+                  balance_grad: Optional[torch.Tensor] = None,
+                  dloss: Optional[torch.Tensor] = None, need_dbias: bool = False,
+                  workspace: Optional[torch.Tensor] = None):
+    """Gradient of moe_route's gate weights (dtopk_w [T, k]) and of moe_balance_loss
+    (balance_grad [B, E], its upstream gradient dloss, one fp32 on the GPU, 1 if None) with
+    respect to the logits.  Returns dlogits [T, E], or (dlogits, dbias [E]) with need_dbias."""
+    fn = "moe_route_bwd"
+    T, E, k, B, mask = _router_args(fn, logits, topk_idx, bias, mask, offsets)
+    dev = logits.device
+    _want(fn, "dtopk_w", dtopk_w, torch.float32, T, k)
+    _want(fn, "balance_grad", balance_grad, torch.float32, B, E)
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+        raise ValueError(f"{fn}: dloss must be one fp32 value")
+    dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    dbias = torch.empty(E, dtype=torch.float32, device=dev) if need_dbias else None
+    if need_dbias and workspace is None:
+        workspace = torch.empty(moe_route_bwd_workspace_size(T, E), dtype=torch.uint8, device=dev)
+    _lib.check(_lib_().moe_route_bwd(_ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(dtopk_w),
+                                     _ptr(mask), _ptr(offsets), _ptr(balance_grad), _ptr(dloss),
+                                     T, E, k, B, MOE_ROUTE_RENORM if renorm else 0, _ptr(dlogits),
+                                     _ptr(dbias), _ptr(workspace),
+                                     _nbytes(workspace),
+                                     _stream(dev)), fn)
+    return (dlogits, dbias) if need_dbias else dlogits
 
 
 # --------------------------------------------------------- measurement probes

@@ -1,4 +1,5 @@
-"""ctypes loader of ``libmoe_gfx950.so`` (the C ABI declared in include/moe.h).
+"""ctypes loader of ``libmoe_gfx950.so`` (the C ABI declared in include/moe.h and
+include/moe_ops.h).
 
 Loading fails loudly when the library has not been built: there is no CPU fallback.
 """
@@ -22,11 +23,14 @@ MOE_EPI_PLAIN, MOE_EPI_SWIGLU = 0, 1
 MOE_MODE_FP32, MOE_MODE_FP8, MOE_MODE_W4A16, MOE_MODE_W4A8 = 0, 1, 2, 3
 MOE_ROUTE_SCORE, MOE_ROUTE_HASH = 0, 1
 MOE_LAYOUT_CONTIGUOUS, MOE_LAYOUT_MASKED = 0, 1
+MOE_BALANCE_SWITCH, MOE_BALANCE_SQUARE = 0, 1
+MOE_FEW_SLOTS_MAX = 1024
 
 _P = C.c_void_p
 _I = C.c_int
 _U = C.c_uint
 _D = C.c_double
+_F = C.c_float
 _Z = C.c_size_t
 
 
@@ -76,6 +80,21 @@ SIGNATURES = {
                                    _P, _P, _Z, _I, _P, _P]),
 }
 
+# the same for include/moe_ops.h
+SIGNATURES_OPS = {
+    "moe_quant_weight_int4_group": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_matvec_int4": (_I, [_P, _I, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _I, _P]),
+    "moe_ffn_int4_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "moe_ffn_int4": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _Z,
+                          _P]),
+    "moe_balance_workspace_size": (_Z, [_I, _I, _I]),
+    "moe_route_bwd_workspace_size": (_Z, [_I, _I]),
+    "moe_balance_loss": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _Z,
+                              _P]),
+    "moe_route_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _U, _P, _P, _P, _Z,
+                           _P]),
+}
+
 _lib = None
 
 
@@ -88,7 +107,7 @@ def load() -> C.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python -m fp8_grouped_gemm_amd.build` (no CPU fallback exists)")
     lib = C.CDLL(LIB_PATH)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in (*SIGNATURES.items(), *SIGNATURES_OPS.items()):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -12,12 +12,18 @@
 #include <cstring>
 
 #include "../../include/moe.h"
+#include "api_common.hpp"
 #include "launch.hpp"
 #include "tiles.hpp"
 
 namespace {
-
 thread_local char g_err[512] = "";
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_dev_ok[kMaxDevices];    // 0 unknown, 1 gfx950, -1 other
+std::atomic<int> g_dev_cus[kMaxDevices];
+}  // namespace
+
+namespace moe {
 
 int fail(int status, const char* fmt, ...) {
   va_list ap;
@@ -26,15 +32,6 @@ int fail(int status, const char* fmt, ...) {
   va_end(ap);
   return status;
 }
-
-#define REQUIRE(cond, ...) \
-  do {                     \
-    if (!(cond)) return fail(MOE_ERR_INVALID_ARG, __VA_ARGS__); \
-  } while (0)
-
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_dev_ok[kMaxDevices];    // 0 unknown, 1 gfx950, -1 other
-std::atomic<int> g_dev_cus[kMaxDevices];
 
 int check_device(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return fail(MOE_ERR_UNSUPPORTED, "device %d out of range", dev);
@@ -52,7 +49,6 @@ int check_device(int dev) {
   return MOE_OK;
 }
 
-// current device must be gfx950; fills the CU count
 int current_device(int* cus) {
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
@@ -67,6 +63,15 @@ int hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return MOE_OK;
   return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace moe
+
+namespace {
+
+using moe::check_device;
+using moe::current_device;
+using moe::fail;
+using moe::hip_status;
 
 inline hipStream_t S(void* s) { return static_cast<hipStream_t>(s); }
 

@@ -91,4 +91,27 @@ hipError_t launch_combine(const void* o, bool o_bf16, const int32_t* row_of_slot
                           const float* w, int T, int k, int d, void* y, bool y_bf16,
                           hipStream_t s);
 
+// ---- operators of include/moe_ops.h
+hipError_t launch_quant_weight_int4_group(const float* w, int G, int N, int K, int group,
+                                          uint8_t* q, float* s7, hipStream_t s);
+// y[s] = matrix of expert idx[s] times x row s / x_div (matvec.hip)
+hipError_t launch_matvec_int4(const void* x, bool x_bf16, int x_div, const uint8_t* q,
+                              const float* s7, int group, const int32_t* idx, int S, int G, int N,
+                              int K, bool swiglu, void* y, bool y_bf16, hipStream_t s);
+// y[t] = sum_j w[t, j] o[t k + j] over the slots with an expert in [0, E)
+hipError_t launch_few_combine(const float* o, const int32_t* idx, const float* w, int T, int k,
+                              int E, int d, void* y, bool y_bf16, hipStream_t s);
+// parts that the tokens of each segment are cut into (balance.hip), and the workspace
+int balance_parts(int T, int B);
+size_t balance_ws_bytes(int T, int E, int B);
+hipError_t launch_balance_loss(const float* logits, const float* bias, const int32_t* idx,
+                               const uint8_t* mask, const int32_t* offsets, int T, int E, int k,
+                               int B, bool square, float coef, int32_t* counts, float* probs,
+                               float* grad, float* loss, void* ws, hipStream_t s);
+int route_bwd_blocks(int T);
+hipError_t launch_route_bwd(const float* logits, const float* bias, const int32_t* idx,
+                            const float* dw, const uint8_t* mask, const int32_t* offsets,
+                            const float* grad, const float* dloss, int T, int E, int k, int B,
+                            bool renorm, float* dlogits, float* dbias, void* ws, hipStream_t s);
+
 }  // namespace moe

@@ -104,6 +104,47 @@ __global__ __launch_bounds__(256) void quant_weight_int4_kernel(const float* __r
   if (li == 0) s7[row * KB + kb] = amax / 7.0f;
 }
 
+// The int4 rule above with blocks of GROUP weights: GROUP / 8 lanes per block.
+template <int GROUP>
+__global__ __launch_bounds__(256) void quant_weight_int4_group_kernel(
+    const float* __restrict__ w, long words, uint8_t* __restrict__ q, float* __restrict__ s7) {
+  constexpr int LG = GROUP / 8;
+  const long p = (long)blockIdx.x * 256 + threadIdx.x;   // one word of 8 codes per lane
+  if (p >= words) return;                                // whole lane groups exit together
+  const v4f a = *reinterpret_cast<const v4f*>(w + p * 8);
+  const v4f b = *reinterpret_cast<const v4f*>(w + p * 8 + 4);
+  float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = group_max<LG>(amax);
+  if (amax == 0.f) amax = 1.f;
+  uint32_t packed = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t = v[i] / amax;
+    t = t * 7.0f;
+    const int qi = (int)rintf(t);
+    const uint32_t nib = qi < 0 ? (8u | (uint32_t)(-qi)) : (uint32_t)qi;
+    packed |= nib << (8 * (i & 3) + 4 * (i >> 2));
+  }
+  reinterpret_cast<uint32_t*>(q)[p] = packed;
+  if (p % LG == 0) s7[p / LG] = amax / 7.0f;
+}
+
+hipError_t launch_quant_weight_int4_group(const float* w, int G, int N, int K, int group,
+                                          uint8_t* q, float* s7, hipStream_t s) {
+  const long words = (long)G * N * (K / 8);
+  const dim3 grid((unsigned)((words + 255) / 256)), block(256);
+  if (group == 32)
+    hipLaunchKernelGGL(quant_weight_int4_group_kernel<32>, grid, block, 0, s, w, words, q, s7);
+  else if (group == 64)
+    hipLaunchKernelGGL(quant_weight_int4_group_kernel<64>, grid, block, 0, s, w, words, q, s7);
+  else
+    hipLaunchKernelGGL(quant_weight_int4_group_kernel<128>, grid, block, 0, s, w, words, q, s7);
+  return hipGetLastError();
+}
+
 hipError_t launch_quant_act(const void* x, bool bf16, int K, const int32_t* src_row, int src_div,
                             int rows_out, uint8_t* q, float* scales, hipStream_t s) {
   const long groups = (long)rows_out * (K / 128);
