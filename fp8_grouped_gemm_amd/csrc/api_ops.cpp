@@ -18,6 +18,8 @@ bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
 size_t align_up(size_t v) { return (v + 255) & ~size_t(255); }
 
+moe::FewDtype few_dt(moe_dtype dt) { return dt == MOE_BF16 ? moe::kFewBf16 : moe::kFewF32; }
+
 bool float_dt(moe_dtype dt) { return dt == MOE_BF16 || dt == MOE_F32; }
 
 int v_group(const char* fn, int group) {
@@ -67,7 +69,8 @@ int moe_matvec_int4(const void* x, moe_dtype x_dt, int x_div, const uint8_t* q, 
   REQUIRE(float_dt(x_dt) && float_dt(y_dt), "moe_matvec_int4: dtypes must be MOE_BF16 or MOE_F32");
   int st = v_group("moe_matvec_int4", group);
   if (st) return st;
-  REQUIRE(x_div >= 1, "moe_matvec_int4: x_div must be >= 1");
+  REQUIRE(x_div >= 1 && (idx || x_div == 1),
+          "moe_matvec_int4: x_div must be >= 1, and 1 without idx (got %d)", x_div);
   REQUIRE(G >= 1 && G <= 65536, "moe_matvec_int4: G must be in [1, 65536] (got %d)", G);
   REQUIRE(N >= 1 && N <= (1 << 24), "moe_matvec_int4: N must be in [1, 2^24] (got %d)", N);
   REQUIRE(K >= group && K % group == 0,
@@ -77,16 +80,16 @@ int moe_matvec_int4(const void* x, moe_dtype x_dt, int x_div, const uint8_t* q, 
   REQUIRE(aligned(x, 16) && aligned(q, 16), "moe_matvec_int4: x and q must be 16-byte aligned");
   if (n_slots == 0) return MOE_OK;
   if ((st = current_device(nullptr))) return st;
-  return hip_status(moe::launch_matvec_int4(x, x_dt == MOE_BF16, x_div, q, s7, group, idx, n_slots,
-                                            G, N, K, epilogue == MOE_EPI_SWIGLU, y,
-                                            y_dt == MOE_BF16, S(stream)),
+  return hip_status(moe::launch_matvec_int4(x, few_dt(x_dt), x_div, q, s7, group, idx, n_slots, G,
+                                            N, K, epilogue == MOE_EPI_SWIGLU, y, few_dt(y_dt),
+                                            S(stream)),
                     "matvec launch");
 }
 
 size_t moe_ffn_int4_workspace_size(int T, int k, int d, int I) {
   if (T <= 0 || k < 1 || d < 1 || I < 1 || (long long)T * k > MOE_FEW_SLOTS_MAX) return 0;
   const size_t slots = (size_t)T * k;
-  return align_up(slots * I * 4) + align_up(slots * d * 4);   // h, o
+  return align_up(slots * I * 6) + align_up(slots * d * 4);   // h in three parts, o
 }
 
 int moe_ffn_int4(const void* x, moe_dtype dt, const uint8_t* w13, const float* s13,
@@ -113,14 +116,14 @@ int moe_ffn_int4(const void* x, moe_dtype dt, const uint8_t* w13, const float* s
     return fail(MOE_ERR_WORKSPACE, "moe_ffn_int4: workspace %zu < %zu bytes", ws_bytes, need);
   if ((st = current_device(nullptr))) return st;
   const int slots = T * k;
-  float* h = static_cast<float*>(ws);
-  float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up((size_t)slots * I * 4));
-  if ((st = hip_status(moe::launch_matvec_int4(x, dt == MOE_BF16, k, w13, s13, group, topk_idx,
-                                               slots, E, I, d, true, h, false, S(stream)),
+  // h is fp32 kept as three bf16 rows a slot, the form the down product multiplies
+  float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up((size_t)slots * I * 6));
+  if ((st = hip_status(moe::launch_matvec_int4(x, few_dt(dt), k, w13, s13, group, topk_idx, slots,
+                                               E, I, d, true, ws, moe::kFewParts, S(stream)),
                        "ffn gate/up launch")))
     return st;
-  if ((st = hip_status(moe::launch_matvec_int4(h, false, 1, w2, s2, group, topk_idx, slots, E, d,
-                                               I, false, o, false, S(stream)),
+  if ((st = hip_status(moe::launch_matvec_int4(ws, moe::kFewParts, 1, w2, s2, group, topk_idx,
+                                               slots, E, d, I, false, o, moe::kFewF32, S(stream)),
                        "ffn down launch")))
     return st;
   return hip_status(moe::launch_few_combine(o, topk_idx, topk_w, T, k, E, d, y, dt == MOE_BF16,

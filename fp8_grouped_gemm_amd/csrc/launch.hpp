@@ -94,10 +94,12 @@ hipError_t launch_combine(const void* o, bool o_bf16, const int32_t* row_of_slot
 // ---- operators of include/moe_ops.h
 hipError_t launch_quant_weight_int4_group(const float* w, int G, int N, int K, int group,
                                           uint8_t* q, float* s7, hipStream_t s);
+// rows of the few-token products: bf16, fp32, or fp32 held as three bf16 rows (3 r + part)
+enum FewDtype { kFewF32, kFewBf16, kFewParts };
 // y[s] = matrix of expert idx[s] times x row s / x_div (matvec.hip)
-hipError_t launch_matvec_int4(const void* x, bool x_bf16, int x_div, const uint8_t* q,
+hipError_t launch_matvec_int4(const void* x, FewDtype x_dt, int x_div, const uint8_t* q,
                               const float* s7, int group, const int32_t* idx, int S, int G, int N,
-                              int K, bool swiglu, void* y, bool y_bf16, hipStream_t s);
+                              int K, bool swiglu, void* y, FewDtype y_dt, hipStream_t s);
 // y[t] = sum_j w[t, j] o[t k + j] over the slots with an expert in [0, E)
 hipError_t launch_few_combine(const float* o, const int32_t* idx, const float* w, int T, int k,
                               int E, int d, void* y, bool y_bf16, hipStream_t s);

@@ -48,7 +48,7 @@ int moe_quant_weight_int4_group(const float *w, int G, int N, int K, int group, 
  *   each); q [G, Nb, K/2] and s7 [G, Nb, K/group] as moe_quant_weight_int4 or
  *   moe_quant_weight_int4_group write them, Nb = N or 2N; group 32, 64 or 128; K a
  *   positive multiple of group; N >= 1; 1 <= G <= 65536; 0 <= S <= MOE_FEW_SLOTS_MAX;
- *   x_div >= 1.  x and q 16-byte aligned.  y must not overlap an input (not checked).
+ *   x_div >= 1 (1 without idx).  x and q 16-byte aligned.  y must not overlap an input (not checked).
  * Two slots may name the same expert (its weights are then read once for up to 16 of
  * them) and the same row. */
 int moe_matvec_int4(const void *x, moe_dtype x_dt, int x_div, const uint8_t *q, const float *s7,
