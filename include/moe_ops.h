@@ -96,8 +96,8 @@ size_t moe_route_bwd_workspace_size(int T, int E);
  *                        (0 if none has)
  * The softmax is the router's (key = fl32(logit + bias), fp32); sums over tokens are
  * carried on in fp64.  -inf logits are experts with probability 0; a token whose logits
- * are all -inf has p = 0.  NaN or +inf in a counting token's row gives NaN probs, grad and
- * loss.  logits [T, E] fp32, bias [E] fp32 or NULL (0), topk_idx [T, k] int32; 1 <= B <=
+ * are all -inf has p = 0.  NaN or +inf in a counting token's row gives NaN probs and loss
+ * (and grad, for MOE_BALANCE_SQUARE).  logits [T, E] fp32, bias [E] fp32 or NULL (0), topk_idx [T, k] int32; 1 <= B <=
  * 65535; pointers to [T, ...] inputs may be NULL when T = 0. */
 int moe_balance_loss(const float *logits, const float *bias, const int32_t *topk_idx,
                      const uint8_t *mask, const int32_t *offsets, int T, int E, int k, int B,
