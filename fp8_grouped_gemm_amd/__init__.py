@@ -41,11 +41,13 @@ def _ptr(t: Optional[torch.Tensor]):
         raise ValueError("tensor must be on the GPU")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(dev: torch.device):
-    return C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    """The handle of torch's current stream on dev (without the Stream object around it)."""
+    i = dev.index if dev.index is not None else torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(i)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -67,15 +69,18 @@ def _on_tensor_device(fn):
     the two must agree; tensors on different GPUs are refused."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        flat = []
+        dev = None
         for a in (*args, *kwargs.values()):
-            flat.extend(a.values() if isinstance(a, dict) else (a,))
-        devs = {a.device for a in flat if isinstance(a, torch.Tensor) and a.is_cuda}
-        if len(devs) > 1:
-            raise ValueError(f"{fn.__name__}: tensors on different devices {sorted(map(str, devs))}")
-        if not devs:
+            for t in (a.values() if isinstance(a, dict) else (a,)):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    if dev is None:
+                        dev = t.device
+                    elif t.device != dev:
+                        raise ValueError(f"{fn.__name__}: tensors on different devices "
+                                         f"{sorted((str(dev), str(t.device)))}")
+        if dev is None or dev.index == torch.cuda.current_device():
             return fn(*args, **kwargs)
-        with torch.cuda.device(devs.pop()):
+        with torch.cuda.device(dev):
             return fn(*args, **kwargs)
     return call
 
