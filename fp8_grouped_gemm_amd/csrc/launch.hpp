@@ -101,6 +101,10 @@ hipError_t launch_matvec_int4(const void* x, FewDtype x_dt, int x_div, const uin
                               const float* s7, int group, const int32_t* idx, int S, int G, int N,
                               int K, bool swiglu, void* y, FewDtype y_dt, hipStream_t s);
 // y[t] = sum_j w[t, j] o[t k + j] over the slots with an expert in [0, E)
+// y[t] = sum over its k slots of w * (down product of the slot's row of h), one launch
+hipError_t launch_join_int4(const void* h, const uint8_t* q, const float* s7, int group,
+                            const int32_t* idx, const float* w, int T, int k, int E, int d, int I,
+                            void* y, bool y_bf16, hipStream_t s);
 hipError_t launch_few_combine(const float* o, const int32_t* idx, const float* w, int T, int k,
                               int E, int d, void* y, bool y_bf16, hipStream_t s);
 // parts that the tokens of each segment are cut into (balance.hip), and the workspace

@@ -6,17 +6,23 @@
 //
 // The weights are the traffic (half a byte per multiplication and row), so each is read
 // once for all slots of its expert and everything else is kept off the memory's way: the
-// codes -7..7 are exact in bf16 and go through the 16x16x32 bf16 matrix instruction with
-// the rows of x, which leaves the vector ALU the expansion of the codes (14 operations per
-// 8 codes) and one multiply-add per group and output.
+// codes go through the 16x16x32 bf16 matrix instruction with the rows of x, which leaves the
+// vector ALU the expansion of the codes (10 operations per 8 codes) and one multiply-add per
+// group and output.
 //
-// A workgroup owns 16 or 32 weight rows of one expert (SwiGLU: 16 gate rows and the 16 up
-// rows of the same outputs); its waves split K into contiguous ranges of 128-deep blocks
-// and join their sums through LDS in wave order.  In the matrix instruction the weights
-// are the right operand (lane l: weight row l % 16), so a lane needs the scale of one row
-// only; up to 16 rows of x are the left one.  A row of x in fp32 is three rows of bf16,
-// its leading, middle and last 8 bits (x = hi + mid + lo exactly), whose sums are added at
-// the end: the products stay exact.
+// A wave takes a tile of 32 or 16 weight rows of one expert (SwiGLU: 16 gate rows and the 16 up
+// rows of the same outputs) and a slice of K in 128-deep blocks, four of them in flight; the
+// slices of a tile are waves of one workgroup and are joined through LDS in slice order.  In
+// the matrix instruction the weights are the right operand (lane l: weight row l % 16), so a
+// lane needs the scale of one row only; up to 16 rows of x are the left one.  A row of x in
+// fp32 is three rows of bf16, its leading, middle and last 8 bits (x = hi + mid + lo exactly),
+// whose sums are added at the end: the products stay exact.
+//
+// Bound by the reading of the weights.  31 of 256 experts' gate and up rows (2 x 2048 x 7168,
+// 485 MB of codes and scales) take 95 us, 5.1 TB/s, where a bare read of such rows in this
+// order takes 87 and a read front to back 75: every row of a tile is a stream of its own.
+// Slices that interleave, workgroups of 8 waves, of runs of tiles or with all eight waves on
+// one tile measured 96 to 108.
 #include <algorithm>
 
 #include "common.hpp"
@@ -27,7 +33,9 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSlots = 1024;
-constexpr int kStageBytes = 8 * 7424;   // LDS for staged x
+// LDS for staged x, per wave: with a slice of K per wave two blocks of 13 rows fit, and the
+// workgroups that the registers allow (16 waves a CU) fit the CU's LDS.
+constexpr int kWaveBytes = 7168;
 constexpr int kRing = 4;                // blocks of codes a wave has in flight (few rows)
 
 __device__ __forceinline__ void store_out(void* y, size_t i, float v, bool bf16) {
@@ -46,6 +54,8 @@ struct MatvecArgs {
   void* y;
   int y_bf16;       // 1: bf16; 0: fp32; 2: fp32 as three bf16 rows (3 s + part)
   int ks_log;       // log2 of the slices of K
+  int k;            // joined form: slots of a token and their weights
+  const float* wgt;
   uint32_t inv_div; // ceil(2^20 / x_div)
 };
 
@@ -146,31 +156,31 @@ __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + expf(-z)
 
 }  // namespace
 
-template <int XF, bool SWIGLU, int R, int GROUP>
-__global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
+// JOIN: the outputs of a token are the sums over its k slots, times the slots' weights, and
+// each slot's product is a wave's (or several waves', over K).
+template <int NW, int XF, bool SWIGLU, int R, int GROUP, bool JOIN>
+__global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
   static_assert(!SWIGLU || R == 2, "SwiGLU: one gate and one up tile");
-  constexpr int NW = 8, NT = NW * 64;
+  constexpr int NT = NW * 64;
   constexpr int RPS = XF == kXBf16 ? 1 : 3;        // left-operand rows per slot
   constexpr int GP = 128 / GROUP;                  // groups per block
   constexpr int NO = SWIGLU ? 16 : 16 * R;         // outputs per wave
-  // staged x: two workgroups' LDS fit a CU beside their scales; with 8 slices of K a slice
-  // has room for two blocks of 14 rows.  A staged row ends 16 bytes off a multiple of the
-  // banks, so that the rows of one read fall into different ones.
-  constexpr int XBYTES = kStageBytes;
+  constexpr int SCH = 16 / GP, SST = 17;           // blocks of staged scales, floats per row
+  constexpr int XBYTES = NW * kWaveBytes;
   static_assert(NW * R * 4 * 64 * 4 <= XBYTES, "the waves' sums reuse the staging region");
   __shared__ uint16_t slots[kMaxSlots];            // slots of the expert
-  __shared__ int wcnt[2][NW];
-  constexpr int SCH = 16 / GP, SST = 17;           // blocks of staged scales, floats per row
+  // A staged row ends 16 bytes off a multiple of the banks, so that the rows of one read fall
+  // into different ones.
   __shared__ __attribute__((aligned(16))) uint8_t xs_mem[XBYTES];
   __shared__ float sc_mem[NW][16 * R * SST];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 4, l16 = lane & 15;
   const int N = a.N, K = a.K, S = a.S;
-  // wave ti * KS + ks: K slice ks of the workgroup's tile ti
+  // wave ti * KS + ks: K slice ks of the workgroup's tile ti (JOIN: of the round's slot ti)
   const int KS = 1 << a.ks_log, TW = NW >> a.ks_log;
   const int ks = wid & (KS - 1), ti = wid >> a.ks_log;
-  const int nb0 = blockIdx.x * (TW * NO), n0 = nb0 + ti * NO;
+  const int nb0 = blockIdx.x * (JOIN ? NO : TW * NO), n0 = nb0 + (JOIN ? 0 : ti * NO);
   const bool y3 = a.y_bf16 == 2;
   auto store = [&](int s, int n, float v) {
     if (y3) {
@@ -182,58 +192,52 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
     }
   };
 
-  // the expert and its slots, in slot order
+  // the expert and its slots, in slot order; every wave finds them for itself, so that the
+  // first weights are asked for before the waves meet
   int e = 0, cnt = S;
-  if (a.idx) {
+  if (!JOIN && a.idx) {
     // S <= G: workgroup row y stands for slot y and works if it is its expert's first slot
     const int me = blockIdx.y;
     const bool by_slot = S <= a.G;
-    int es = a.idx[min(tid, S - 1)];
+    int es = a.idx[min(lane, S - 1)];
     e = __builtin_amdgcn_readfirstlane(by_slot ? a.idx[me] : me);
     const bool live = e >= 0 && e < a.G;
     if (!live && me != 0) return;
     cnt = 0;
-    for (int s0 = 0, turn = 0; s0 < S; s0 += NT, turn ^= 1) {
-      const int s = s0 + tid;
+    int first = S;
+    for (int s0 = 0; s0 < S; s0 += 64) {
+      const int s = s0 + lane;
       if (s0 > 0) es = a.idx[min(s, S - 1)];
-      const bool mine = s < S && es == e;
-      if (me == 0 && blockIdx.z == 0 && (es < 0 || es >= a.G) && s < S)   // no expert: zeros
+      const unsigned long long m = __ballot(s < S && es == e);
+      if (m && first == S) first = s0 + __builtin_ctzll(m);
+      if (wid == 0 && s < S) {
+        if (me == 0 && blockIdx.z == 0 && (es < 0 || es >= a.G))   // no expert: zeros
 #pragma unroll 1
-        for (int c = 0; c < min(TW * NO, N - nb0); ++c) store(s, nb0 + c, 0.f);
-      const unsigned long long m = __ballot(mine);
-      if (lane == 0) wcnt[turn][wid] = __popcll(m);
-      __syncthreads();
-      int at = cnt;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        if (w < wid) at += wcnt[turn][w];
-        cnt += wcnt[turn][w];
+          for (int c = 0; c < min(TW * NO, N - nb0); ++c) store(s, nb0 + c, 0.f);
+        if (es == e) slots[cnt + __popcll(m & ((1ull << lane) - 1ull))] = (uint16_t)s;
       }
-      if (mine) slots[at + __popcll(m & ((1ull << lane) - 1ull))] = (uint16_t)s;
+      cnt += __popcll(m);
     }
-    __syncthreads();
-    if (!live) return;
-    // (readfirstlane: the whole workgroup agrees, which the compiler cannot see in LDS)
-    cnt = __builtin_amdgcn_readfirstlane(cnt);
-    if (cnt == 0 || (by_slot && __builtin_amdgcn_readfirstlane((int)slots[0]) != me)) return;
+    if (!live || cnt == 0 || (by_slot && first != me)) return;
   }
 
   // weight rows of the wave's tiles and their scales, bounded by their buffers: rows past N
-  // read as zeros and are not stored
+  // (and all rows of a slot without an expert) read as zeros and are not stored
   const int KG = K / GROUP;
-  const int last = N - 1 - n0;                       // < 0: the wave has no rows
   __amdgpu_buffer_rsrc_t wbuf[R], sbuf[R];
+  auto rows_of = [&](int expert, int limit) {
 #pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const int first = SWIGLU ? 0 : 16 * t;
-    const int rows = __builtin_amdgcn_readfirstlane(max(min(16, last + 1 - first), 0));
-    const size_t row0 = (size_t)e * (SWIGLU ? 2 * (size_t)N : N) + (SWIGLU ? (size_t)t * N : 0) +
-                        (rows ? n0 + first : 0);
-    wbuf[t] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.q + row0 * (K / 2)),
-                                                (short)0, rows * (K / 2), 0x00020000);
-    sbuf[t] = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.s7 + row0 * KG), (short)0,
-                                                rows * KG * 4, 0x00020000);
-  }
+    for (int t = 0; t < R; ++t) {
+      const int n = n0 + (SWIGLU ? 0 : 16 * t);
+      const int rows = __builtin_amdgcn_readfirstlane(max(min(16, limit - n), 0));
+      const size_t row0 = (size_t)expert * (SWIGLU ? 2 * (size_t)N : N) +
+                          (SWIGLU ? (size_t)t * N : 0) + (rows ? n : 0);
+      wbuf[t] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.q + row0 * (K / 2)),
+                                                  (short)0, rows * (K / 2), 0x00020000);
+      sbuf[t] = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.s7 + row0 * KG), (short)0,
+                                                  rows * KG * 4, 0x00020000);
+    }
+  };
   constexpr uint32_t kNowhere = 0xFFFFFF00u;          // a lane offset beyond every bound
   const int KB = (K + 127) / 128;
   const int b0 = (int)(((long)ks * KB) >> a.ks_log), b1 = (int)(((long)(ks + 1) * KB) >> a.ks_log);
@@ -249,41 +253,43 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
       w[t] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(wbuf[t], at, 0, 0));
   };
   // Scales of SCH blocks from kb on, 16 groups of a row: a lane takes 4 groups of row lane / 4
-  // (64 contiguous bytes a row), and from a short row's end 4 groups that begin earlier.  They
-  // wait in registers while the blocks before them are computed and then move to LDS.
+  // (64 contiguous bytes a row).  They wait in registers while the blocks before them are
+  // computed and then move to LDS, with zeros behind the row's last group.
   float* sc = sc_mem[wid];
-  auto scale_at = [&](int kb) { return min(kb * GP + 4 * (lane & 3), max(KG - 4, 0)); };
   auto load_s = [&](v4f (&sv)[R], int kb) {
-    const uint32_t at = (uint32_t)((lane >> 2) * KG + scale_at(kb)) * 4u;
+    const int g = kb * GP + 4 * (lane & 3);
+    const uint32_t at = g < b1 * GP ? (uint32_t)((lane >> 2) * KG + g) * 4u : kNowhere;
 #pragma unroll
-    for (int t = 0; t < R; ++t) {
-      if (KG >= 4) {
-        sv[t] = __builtin_bit_cast(
-            v4f, __builtin_amdgcn_raw_buffer_load_b128(sbuf[t], kb < b1 ? at : kNowhere, 0, 0));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sv[t][j] = __builtin_bit_cast(
-              float, __builtin_amdgcn_raw_buffer_load_b32(
-                         sbuf[t], j < KG && kb < b1 ? at + 4u * j : kNowhere, 0, 0));
-      }
-    }
+    for (int t = 0; t < R; ++t)
+      sv[t] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(sbuf[t], at, 0, 0));
   };
   auto put_s = [&](const v4f (&sv)[R], int kb) {
-    const int at = scale_at(kb) - kb * GP;             // may begin before the chunk
+    const int left = KG - (kb * GP + 4 * (lane & 3));
 #pragma unroll
     for (int t = 0; t < R; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (at + j >= 0) sc[(16 * t + (lane >> 2)) * SST + at + j] = sv[t][j];
+      for (int i = 0; i < 4; ++i)
+        sc[(16 * t + (lane >> 2)) * SST + 4 * (lane & 3) + i] = i < left ? sv[t][i] : 0.f;
   };
 
-  // slots per pass: 16 rows, or what two blocks of a slice's staging region hold
-  const int room = (XBYTES >> a.ks_log) & ~15;
-  const int spp = min(16, room / (2 * 256 + 16)) / RPS;
-  for (int s0 = blockIdx.z * spp; s0 < cnt; s0 += gridDim.z * spp) {
-    const int ns = min(spp, cnt - s0), nr = ns * RPS;
-    auto slot_at = [&](int i) { return a.idx ? (int)slots[s0 + i] : s0 + i; };
+  // slots per pass: 16 rows, or what two blocks of a slice's staging region hold.  JOIN: the
+  // waves' next slots of the token, one row each, staged by the wave itself
+  const int room = JOIN ? kWaveBytes : (XBYTES >> a.ks_log) & ~15;
+  const int spp = JOIN ? TW : min(16, room / (2 * 256 + 16)) / RPS;
+  const int s_end = JOIN ? a.k : cnt, s_step = JOIN ? TW : gridDim.z * spp;
+  const int stage_i = JOIN ? 0 : ti, stage_n = JOIN ? 1 : TW;
+  float tot[R] = {};
+  if (!JOIN) rows_of(e, N);
+  for (int s0 = JOIN ? 0 : blockIdx.z * spp; s0 < s_end; s0 += s_step) {
+    const int ns = JOIN ? 1 : min(spp, cnt - s0), nr = ns * RPS;
+    const int own = JOIN ? (int)blockIdx.y * a.k + min(s0 + ti, a.k - 1) : 0;
+    bool valid = true;
+    if constexpr (JOIN) {
+      e = a.idx[own];
+      valid = s0 + ti < a.k && e >= 0 && e < a.G;
+      rows_of(valid ? e : 0, valid ? N : 0);
+    }
+    auto slot_at = [&](int i) { return JOIN ? own : a.idx ? (int)slots[s0 + i] : s0 + i; };
     // slot / x_div by a multiplication: exact for slots below 1024
     auto x_row = [&](int slot) { return (size_t)(((uint32_t)slot * a.inv_div) >> 20); };
     v4f acc[R];
@@ -293,17 +299,17 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
     auto run = [&](auto MRC) {
       constexpr int MR = decltype(MRC)::value;
       constexpr int U = MR == 1 ? kRing : 2;
-      static_assert(4 * (U * 256 + 16) * NW <= XBYTES || MR > 1, "room for a chunk of U blocks");
+      static_assert(4 * (U * 256 + 16) <= kWaveBytes || MR > 1, "room for a chunk of U blocks");
       static_assert(SCH % U == 0, "the ring's turns end with the staged scales");
       // blocks of a chunk, a multiple of the ring's; bytes per staged row and per slice
       const int ch = min((room / nr - 16) / 256, max(nb_max + U - 1, U)) / U * U;
       const int xst = ch * 256 + 16;
-      uint8_t* xs = xs_mem + ks * room;
+      uint8_t* xs = xs_mem + (JOIN ? wid : ks) * room;
       // left-operand row i sits at matrix row 4 (i % 4) + i / 4, so that up to four rows
       // leave each lane one sum; rows past nr repeat the last one
       const uint8_t* xlane = xs + min((l16 >> 2) + 4 * (l16 & 3), nr - 1) * xst;
 
-      // x rows of the blocks [c0, c0 + n) of this slice by the slice's TW waves, zeros past K
+      // x rows of the blocks [c0, c0 + n) of this slice by the slice's waves, zeros past K
       // and in the blocks that fill up the ring's last turn; all loads of a turn are issued
       // before the first is waited for
       auto stage = [&](int c0, int n) {
@@ -311,12 +317,12 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
         const int nu = (XF == kXF32 ? ns : nr) * nb;   // 16-lane units: a row's block
         const float inv = 1.0f / (float)nb;
         constexpr int XV = XF == kXF32 ? 2 : 1, TURN = 4 / XV;
-        for (int u0 = ti * 4; u0 < nu; u0 += TW * 4 * TURN) {
+        for (int u0 = stage_i * 4; u0 < nu; u0 += stage_n * 4 * TURN) {
           v4i v[TURN][XV];
           int dst[TURN];
 #pragma unroll
           for (int j = 0; j < TURN; ++j) {
-            const int u = u0 + TW * 4 * j + h;
+            const int u = u0 + stage_n * 4 * j + h;
             const int i = (int)(((float)u + 0.5f) * inv), blk = u - i * nb;
             const int k = (c0 + blk) * 128 + 8 * l16;
             dst[j] = u < nu ? (XF == kXF32 ? 3 * i : i) * xst + blk * 256 + 16 * l16 : -1;
@@ -386,6 +392,7 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
         load_w(ring[u], b0 + u);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (!JOIN && a.idx && s0 == (int)blockIdx.z * spp) __syncthreads();   // slots
       for (int c = 0; c < nb_max; c += ch) {
         const int c0 = b0 + c, nb = min(ch, b1 - c0);
         if (c > 0) __syncthreads();                    // every wave is done with the chunk
@@ -406,6 +413,7 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
           }
         }
       }
+      if constexpr (JOIN) return;
       __syncthreads();
       float* red = reinterpret_cast<float*>(xs_mem) + wid * (R * 4 * 64);
 #pragma unroll
@@ -413,17 +421,23 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
 #pragma unroll
         for (int r = 0; r < MR; ++r) red[(t * 4 + r) * 64 + lane] = acc[t][r];
     };
-    if (nr <= 4)
+    if constexpr (JOIN) {
       run(std::integral_constant<int, 1>{});
-    else
+#pragma unroll
+      for (int t = 0; t < R; ++t) tot[t] = valid ? fmaf(a.wgt[own], acc[t][0], tot[t]) : tot[t];
+      continue;
+    } else if (nr <= 4) {
+      run(std::integral_constant<int, 1>{});
+    } else {
       run(std::integral_constant<int, 4>{});
+    }
     __syncthreads();
 
     // outputs: row i's sum over the slices sits in lanes 16 (i % 4) + n, register i / 4
     const float* red = reinterpret_cast<const float*>(xs_mem);
     for (int o = tid; o < ns * TW * NO; o += NT) {
       const int c = o % NO, w0 = ((o / NO) & (TW - 1)) << a.ks_log;
-      const int sl = (o / NO) >> (3 - a.ks_log), n = nb0 + o % (TW * NO);
+      const int sl = (o / NO) / TW, n = nb0 + o % (TW * NO);
       float v[2] = {0.f, 0.f};
 #pragma unroll
       for (int t2 = 0; t2 < (SWIGLU ? 2 : 1); ++t2) {
@@ -440,6 +454,24 @@ __global__ __launch_bounds__(512, 4) void matvec_int4_kernel(MatvecArgs a) {
       if (n < N) store(slot_at(sl), n, SWIGLU ? silu_f32(v[0]) * v[1] : v[0]);
     }
     __syncthreads();
+  }
+  if constexpr (JOIN) {
+    // row p of the staged three is a slot's part p: lanes 16 p + n
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(xs_mem);
+#pragma unroll
+    for (int t = 0; t < R; ++t) red[(wid * R + t) * 64 + lane] = tot[t];
+    __syncthreads();
+    if (tid < NO && nb0 + tid < N) {
+      float v = 0.f;
+#pragma unroll
+      for (int p = RPS - 1; p >= 0; --p) {
+        float z = 0.f;
+        for (int w = 0; w < NW; ++w) z += red[(w * R + (tid >> 4)) * 64 + 16 * p + (tid & 15)];
+        v += z;
+      }
+      store((int)blockIdx.y, nb0 + tid, v * kCodeUnit);
+    }
   }
 }
 
@@ -458,50 +490,74 @@ __global__ __launch_bounds__(256) void few_combine_kernel(const float* __restric
   store_out(y, (size_t)t * d + n, acc, y_bf16);
 }
 
-template <int XF, int GROUP>
-hipError_t launch_matvec_xg(MatvecArgs a, bool swiglu, hipStream_t s) {
-  const unsigned gy = a.idx ? (unsigned)(a.S <= a.G ? a.S : a.G) : 1u;
-  const dim3 block(512);
-  const long tiles = ((long)a.N + (swiglu ? 15 : 31)) / (swiglu ? 16 : 32) * gy;
-  // Enough waves for the chip: K in 2 slices from 1024 wave tiles on, 4 from 512, else 8.
-  // (8 experts' gate and up products, 7168 x 4096 each, 1024 tiles, with their down products:
-  // 51 us with 2 slices, 58 with 4, 74 with 8; 30 experts' gate and up: 96, 101, 118.  One
-  // slice measured 67 and 98: its workgroups are too few to even out over the CUs.)
-  a.ks_log = tiles >= 1024 ? 1 : tiles >= 512 ? 2 : 3;
-  // 16-row tiles where 32-row ones would leave CUs idle
-  const bool narrow = !swiglu && tiles < 256;
-  const int per = (swiglu || narrow ? 16 : 32) * (8 >> a.ks_log);
+template <int XF, bool SWIGLU, int R, int GROUP>
+hipError_t launch_matvec_r(const MatvecArgs& a, unsigned gy, hipStream_t s) {
+  constexpr int NW = 4;
+  const int per = (SWIGLU ? 16 : 16 * R) * (NW >> a.ks_log);
   const unsigned gx = (unsigned)((a.N + per - 1) / per);
   // with few workgroups the passes over an expert's slots run beside each other
-  const int spp = std::min(16, (kStageBytes >> a.ks_log) / 528) / (XF == kXBf16 ? 1 : 3);
+  const int spp = std::min(16, (NW * kWaveBytes >> a.ks_log) / 528) / (XF == kXBf16 ? 1 : 3);
   const unsigned gz = (unsigned)std::max<long>(
       1, std::min<long>((a.S + spp - 1) / spp, 512 / ((long)gx * gy)));
-  const dim3 grid(gx, gy, gz);
-  if (swiglu)
-    hipLaunchKernelGGL((matvec_int4_kernel<XF, true, 2, GROUP>), grid, block, 0, s, a);
-  else if (narrow)
-    hipLaunchKernelGGL((matvec_int4_kernel<XF, false, 1, GROUP>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((matvec_int4_kernel<XF, false, 2, GROUP>), grid, block, 0, s, a);
+  hipLaunchKernelGGL((matvec_int4_kernel<NW, XF, SWIGLU, R, GROUP, false>), dim3(gx, gy, gz),
+                     dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int XF, int GROUP>
+hipError_t launch_matvec_g(MatvecArgs a, bool swiglu, hipStream_t s) {
+  const unsigned gy = a.idx ? (unsigned)(a.S <= a.G ? a.S : a.G) : 1u;
+  const long tiles = ((long)a.N + (swiglu ? 15 : 31)) / (swiglu ? 16 : 32) * gy;
+  // Enough waves for the chip, in slices long enough to stream: K whole for short rows of
+  // which there are many (101 experts' down products, 7168 x 2048 each: 165 us, in 2 slices
+  // 182), in 2 slices from 1024 wave tiles on (8 experts' gate and up products, 2 x 2048 x
+  // 7168 each: 30.5 us, in 4 slices 32.5; 101 experts': 300 us, whole 317), else in 4.
+  a.ks_log = tiles >= 2048 && a.K <= 2048 ? 0 : tiles >= 1024 ? 1 : 2;
+  if (swiglu) {
+    if constexpr (XF == kXParts)
+      return hipErrorInvalidValue;                   // (no caller has such rows)
+    else
+      return launch_matvec_r<XF, true, 2, GROUP>(a, gy, s);
+  }
+  // 16-row tiles where 32-row ones would leave CUs idle
+  return tiles < 256 ? launch_matvec_r<XF, false, 1, GROUP>(a, gy, s)
+                     : launch_matvec_r<XF, false, 2, GROUP>(a, gy, s);
+}
+
+template <int GROUP>
+hipError_t launch_join_g(MatvecArgs a, int T, hipStream_t s) {
+  constexpr int NW = 8;
+  a.ks_log = a.k > 4 ? 0 : a.k > 2 ? 1 : a.k > 1 ? 2 : 3;
+  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)T), block(64 * NW);
+  hipLaunchKernelGGL((matvec_int4_kernel<NW, kXParts, false, 1, GROUP, true>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 template <int XF>
 hipError_t launch_matvec_x(const MatvecArgs& a, int group, bool swiglu, hipStream_t s) {
-  return group == 32   ? launch_matvec_xg<XF, 32>(a, swiglu, s)
-         : group == 64 ? launch_matvec_xg<XF, 64>(a, swiglu, s)
-                       : launch_matvec_xg<XF, 128>(a, swiglu, s);
+  return group == 32   ? launch_matvec_g<XF, 32>(a, swiglu, s)
+         : group == 64 ? launch_matvec_g<XF, 64>(a, swiglu, s)
+                       : launch_matvec_g<XF, 128>(a, swiglu, s);
 }
 
 hipError_t launch_matvec_int4(const void* x, FewDtype x_dt, int x_div, const uint8_t* q,
                               const float* s7, int group, const int32_t* idx, int S, int G, int N,
                               int K, bool swiglu, void* y, FewDtype y_dt, hipStream_t s) {
   const MatvecArgs a{x, q, s7, idx, S, G, N, K, y,
-                     y_dt == kFewBf16 ? 1 : y_dt == kFewParts ? 2 : 0, 0,
+                     y_dt == kFewBf16 ? 1 : y_dt == kFewParts ? 2 : 0, 0, 0, nullptr,
                      (uint32_t)(((1u << 20) + (uint32_t)x_div - 1) / (uint32_t)x_div)};
   return x_dt == kFewBf16    ? launch_matvec_x<kXBf16>(a, group, swiglu, s)
          : x_dt == kFewParts ? launch_matvec_x<kXParts>(a, group, swiglu, s)
                              : launch_matvec_x<kXF32>(a, group, swiglu, s);
+}
+
+hipError_t launch_join_int4(const void* h, const uint8_t* q, const float* s7, int group,
+                            const int32_t* idx, const float* w, int T, int k, int E, int d, int I,
+                            void* y, bool y_bf16, hipStream_t s) {
+  const MatvecArgs a{h, q, s7, idx, T * k, E, d, I, y, y_bf16 ? 1 : 0, 0, k, w, 1u << 20};
+  return group == 32   ? launch_join_g<32>(a, T, s)
+         : group == 64 ? launch_join_g<64>(a, T, s)
+                       : launch_join_g<128>(a, T, s);
 }
 
 hipError_t launch_few_combine(const float* o, const int32_t* idx, const float* w, int T, int k,

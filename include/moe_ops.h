@@ -47,7 +47,8 @@ int moe_quant_weight_int4_group(const float *w, int G, int N, int K, int group, 
  *   x [ceil(S / x_div), K] of dtype x_dt and y [S, N] of dtype y_dt (MOE_BF16 or MOE_F32
  *   each); q [G, Nb, K/2] and s7 [G, Nb, K/group] as moe_quant_weight_int4 or
  *   moe_quant_weight_int4_group write them, Nb = N or 2N; group 32, 64 or 128; K a
- *   positive multiple of group; N >= 1; 1 <= G <= 65536; 0 <= S <= MOE_FEW_SLOTS_MAX;
+ *   positive multiple of group, K <= 2^24; 1 <= N <= 2^24; 1 <= G <= 65536;
+ *   0 <= S <= MOE_FEW_SLOTS_MAX;
  *   x_div >= 1 (1 without idx).  x and q 16-byte aligned.  y must not overlap an input (not checked).
  * Two slots may name the same expert (its weights are then read once for up to 16 of
  * them) and the same row. */
@@ -66,7 +67,7 @@ size_t moe_ffn_int4_workspace_size(int T, int k, int d, int I);
  *   x [T, d] and y [T, d] of dtype dt (MOE_BF16 or MOE_F32); w13 [E, 2I, d/2] (rows [0, I)
  *   gate, [I, 2I) up), s13 [E, 2I, d/group]; w2 [E, d, I/2], s2 [E, d, I/group]; topk_idx
  *   [T, k] int32, topk_w [T, k] fp32 as moe_route writes them; d and I positive multiples
- *   of group (32, 64 or 128); T >= 0, T * k <= MOE_FEW_SLOTS_MAX; 1 <= E <= 65536;
+ *   of group (32, 64 or 128), at most 2^24; T >= 0, T * k <= MOE_FEW_SLOTS_MAX; 1 <= E <= 65536;
  *   x, w13, w2 and ws 16-byte aligned; ws_bytes >= moe_ffn_int4_workspace_size(). */
 int moe_ffn_int4(const void *x, moe_dtype dt, const uint8_t *w13, const float *s13,
                  const uint8_t *w2, const float *s2, int group, const int32_t *topk_idx,

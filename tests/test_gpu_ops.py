@@ -246,6 +246,51 @@ def test_ffn(T, k, E, d, I, group, dt):
     assert torch.equal(M.moe_ffn_int4(*args, workspace=ws), got)
 
 
+@pytest.mark.parametrize("T, k, E, d, I, group", [
+    # one token: 1, 2, 4 and 8 waves a slot, rounds of eight slots, ends of K inside a slice
+    (1, 1, 3, 1056, 2080, 32), (1, 2, 9, 320, 1984, 64), (1, 3, 9, 128, 384, 128),
+    (1, 4, 9, 224, 4128, 32), (1, 5, 9, 64, 64, 64), (1, 9, 12, 192, 896, 64),
+    (1, 16, 16, 160, 32, 32), (1, 17, 20, 384, 1152, 128),
+    # many: gathered by expert
+    (64, 8, 4, 256, 256, 64), (200, 2, 3, 224, 416, 32), (24, 1, 6, 1152, 640, 128),
+    (2, 3, 5, 2080, 2080, 32),
+])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ffn_of_one_token_and_of_many(T, k, E, d, I, group, dt):
+    test_ffn(T, k, E, d, I, group, dt)
+
+
+def test_ffn_of_one_token_without_an_expert():
+    note("ffn one token, dropped")
+    r = gen(77)
+    w13, s13 = weights(r, 4, 128, 64, 32)
+    w2, s2 = weights(r, 4, 64, 64, 32)
+    idx = t_(np.array([[4, -1, 2 ** 31 - 1]], np.int32))
+    x = torch.full((1, 64), float("nan"), device=dev())
+    y = M.moe_ffn_int4(x, t_(w13), t_(s13), t_(w2), t_(s2), idx,
+                       torch.full((1, 3), float("nan"), device=dev()))
+    assert torch.all(y == 0)
+
+
+@pytest.mark.parametrize("K, group", [(32, 32), (160, 32), (640, 128), (896, 128), (1088, 64)])
+def test_matvec_scales_of_an_earlier_call_do_not_linger(K, group):
+    """Blocks behind a row's end multiply zeros, whatever scales the shared memory still holds:
+    here those of a call that left NaN and infinities in all of it."""
+    note(f"matvec lingering scales K={K} group={group}")
+    r = gen(K)
+    q, s = weights(r, 1, 4096, 2048, 32)
+    bad = np.full_like(s, np.nan)
+    bad[:, ::2] = np.inf
+    qk, sk = weights(r, 1, 300, K, group)
+    x, x64 = rows(r, 1, K, torch.bfloat16)
+    v, absum = OP.matvec_int4(x64, OP.int4_weight(qk, sk), None, 1)
+    args = (x, t_(qk), t_(sk))
+    first = (t_(np.zeros((1, 2048), np.float32), torch.bfloat16), t_(q), t_(bad))
+    M.moe_matvec_int4(*first)
+    y = M.moe_matvec_int4(*args)
+    check(y, v, sum_error(absum, K, group))
+
+
 # ---------------------------------------------------------------- balance loss
 
 P_ERR = 2.0 ** -17   # fp32 softmax and sums: 12 u |key - max| + 28 u, then up to 67 additions

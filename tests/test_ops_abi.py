@@ -46,7 +46,7 @@ def _matvec(x=FAKE, x_dt=BF16, x_div=1, q=FAKE, s7=FAKE, group=128, idx=FAKE, S=
     ({"K": -128}, "multiple of group"), ({"N": 0}, "N must"), ({"N": (1 << 24) + 1}, "N must"),
     ({"G": 0}, "G must"), ({"S": -1}, "S must"), ({"S": 1025}, "grouped GEMMs"),
     ({"x_div": 0}, "x_div"), ({"epi": 2}, "epilogue"), ({"x": ODD}, "aligned"),
-    ({"q": ODD}, "aligned"),
+    ({"q": ODD}, "aligned"), ({"idx": None, "x_div": 2}, "x_div"), ({"K": 1 << 25}, "K must"),
 ])
 def test_matvec_refuses(kw, fragment):
     _err(_matvec(**kw), fragment)
