@@ -69,19 +69,28 @@ def _on_tensor_device(fn):
     the two must agree; tensors on different GPUs are refused."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        dev = None
+        index = -1
         for a in (*args, *kwargs.values()):
-            for t in (a.values() if isinstance(a, dict) else (a,)):
-                if isinstance(t, torch.Tensor) and t.is_cuda:
-                    if dev is None:
-                        dev = t.device
-                    elif t.device != dev:
-                        raise ValueError(f"{fn.__name__}: tensors on different devices "
-                                         f"{sorted((str(dev), str(t.device)))}")
-        if dev is None or dev.index == torch.cuda.current_device():
+            if isinstance(a, torch.Tensor):
+                i = a.get_device()                  # -1 for a host tensor
+                if i != index and i >= 0:
+                    if index >= 0:
+                        refuse(index, i)
+                    index = i
+            elif isinstance(a, dict):
+                for t in a.values():
+                    if isinstance(t, torch.Tensor) and t.is_cuda:
+                        if index >= 0 and t.get_device() != index:
+                            refuse(index, t.get_device())
+                        index = t.get_device()
+        if index < 0 or index == torch._C._cuda_getDevice():
             return fn(*args, **kwargs)
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             return fn(*args, **kwargs)
+
+    def refuse(*indices):
+        raise ValueError(f"{fn.__name__}: tensors on different devices "
+                         f"{sorted(f'cuda:{i}' for i in indices)}")
     return call
 
 
