@@ -40,16 +40,16 @@ int moe_quant_weight_int4_group(const float *w, int G, int N, int K, int group, 
  *   v[s, n] = sum_g s7[e, n, g] * ( sum_{k in group g} q[e, n, k] * x[s / x_div, k] )
  *   MOE_EPI_PLAIN:  y[s, n] = v[s, n],                                 n < N
  *   MOE_EPI_SWIGLU: y[s, n] = silu(v[s, n]) * v[s, N + n]   (2N weight rows), n < N
- * The products q x are exact, the sums and the SwiGLU are taken in fp32, and y is rounded
- * once.  The weights are used as q * s7 (grouped_gemm_w4a16 rounds that product to bf16
+ * The products q x are exact (below 2^-115 in magnitude to a multiple of 2^-139), the sums
+ * and the SwiGLU are taken in fp32, and y is rounded once.  The weights are used as q * s7 (grouped_gemm_w4a16 rounds that product to bf16
  * first).  A slot whose expert lies outside [0, G) (a dropped slot, a padding row) gets
  * a row of zeros and its x row is not used.
  *   x [ceil(S / x_div), K] of dtype x_dt and y [S, N] of dtype y_dt (MOE_BF16 or MOE_F32
  *   each); q [G, Nb, K/2] and s7 [G, Nb, K/group] as moe_quant_weight_int4 or
  *   moe_quant_weight_int4_group write them, Nb = N or 2N; group 32, 64 or 128; K a
  *   positive multiple of group, K <= 2^24; 1 <= N <= 2^24; 1 <= G <= 65536;
- *   0 <= S <= MOE_FEW_SLOTS_MAX;
- *   x_div >= 1 (1 without idx).  x and q 16-byte aligned.  y must not overlap an input (not checked).
+ *   0 <= S <= MOE_FEW_SLOTS_MAX; x_div >= 1 (1 without idx).  x and q 16-byte aligned.  y
+ *   must not overlap an input (not checked).
  * Two slots may name the same expert (its weights are then read once for up to 16 of
  * them) and the same row. */
 int moe_matvec_int4(const void *x, moe_dtype x_dt, int x_div, const uint8_t *q, const float *s7,
@@ -62,13 +62,14 @@ size_t moe_ffn_int4_workspace_size(int T, int k, int d, int I);
 /* The routed experts' FFN of a few tokens with 4-bit weights, after the router:
  *   y[t] = sum_j topk_w[t, j] * W2_e ( silu(Wgate_e x_t) * (Wup_e x_t) ),  e = topk_idx[t, j]
  * with the products of moe_matvec_int4; the SwiGLU output stays in fp32, the k terms are
- * added in fp32 in the order j = 0..k-1, and y is rounded once.  Slots whose expert lies
+ * added in fp32 in an order fixed by the sizes, and y is rounded once.  Slots whose expert lies
  * outside [0, E) are skipped (their weight is not used); a token without any gets zeros.
  *   x [T, d] and y [T, d] of dtype dt (MOE_BF16 or MOE_F32); w13 [E, 2I, d/2] (rows [0, I)
  *   gate, [I, 2I) up), s13 [E, 2I, d/group]; w2 [E, d, I/2], s2 [E, d, I/group]; topk_idx
  *   [T, k] int32, topk_w [T, k] fp32 as moe_route writes them; d and I positive multiples
  *   of group (32, 64 or 128), at most 2^24; T >= 0, T * k <= MOE_FEW_SLOTS_MAX; 1 <= E <= 65536;
- *   x, w13, w2 and ws 16-byte aligned; ws_bytes >= moe_ffn_int4_workspace_size(). */
+ *   x, w13, w2 and ws 16-byte aligned; ws_bytes >= moe_ffn_int4_workspace_size().  y must
+ *   not overlap an input (not checked). */
 int moe_ffn_int4(const void *x, moe_dtype dt, const uint8_t *w13, const float *s13,
                  const uint8_t *w2, const float *s2, int group, const int32_t *topk_idx,
                  const float *topk_w, int T, int k, int E, int d, int I, void *y, void *ws,
@@ -98,8 +99,8 @@ size_t moe_route_bwd_workspace_size(int T, int E);
  * The softmax is the router's (key = fl32(logit + bias), fp32); sums over tokens are
  * carried on in fp64.  -inf logits are experts with probability 0; a token whose logits
  * are all -inf has p = 0.  NaN or +inf in a counting token's row gives NaN probs and loss
- * (and grad, for MOE_BALANCE_SQUARE).  logits [T, E] fp32, bias [E] fp32 or NULL (0), topk_idx [T, k] int32; 1 <= B <=
- * 65535; pointers to [T, ...] inputs may be NULL when T = 0. */
+ * (and grad, for MOE_BALANCE_SQUARE).  logits [T, E] fp32, bias [E] fp32 or NULL (0),
+ * topk_idx [T, k] int32; 1 <= B <= 65535; pointers to [T, ...] inputs may be NULL when T = 0. */
 int moe_balance_loss(const float *logits, const float *bias, const int32_t *topk_idx,
                      const uint8_t *mask, const int32_t *offsets, int T, int E, int k, int B,
                      int kind, float coef, int32_t *counts, float *probs, float *grad,
