@@ -54,6 +54,7 @@ struct MatvecArgs {
   void* y;
   int y_bf16;       // 1: bf16; 0: fp32; 2: fp32 as three bf16 rows (3 s + part)
   int ks_log;       // log2 of the slices of K
+  int spp;          // slots of a pass
   int k;            // joined form: slots of a token and their weights
   const float* wgt;
   uint32_t inv_div; // ceil(2^20 / x_div)
@@ -272,10 +273,10 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
         sc[(16 * t + (lane >> 2)) * SST + 4 * (lane & 3) + i] = i < left ? sv[t][i] : 0.f;
   };
 
-  // slots per pass: 16 rows, or what two blocks of a slice's staging region hold.  JOIN: the
-  // waves' next slots of the token, one row each, staged by the wave itself
+  // spp slots a pass.  JOIN: the waves' next slots of the token, one each, whose rows the wave
+  // stages by itself
   const int room = JOIN ? kWaveBytes : (XBYTES >> a.ks_log) & ~15;
-  const int spp = JOIN ? TW : min(16, room / (2 * 256 + 16)) / RPS;
+  const int spp = JOIN ? TW : a.spp;
   const int s_end = JOIN ? a.k : cnt, s_step = JOIN ? TW : gridDim.z * spp;
   const int stage_i = JOIN ? 0 : ti, stage_n = JOIN ? 1 : TW;
   float tot[R] = {};
@@ -491,14 +492,20 @@ __global__ __launch_bounds__(256) void few_combine_kernel(const float* __restric
 }
 
 template <int XF, bool SWIGLU, int R, int GROUP>
-hipError_t launch_matvec_r(const MatvecArgs& a, unsigned gy, hipStream_t s) {
+hipError_t launch_matvec_r(MatvecArgs a, unsigned gy, hipStream_t s) {
   constexpr int NW = 4;
   const int per = (SWIGLU ? 16 : 16 * R) * (NW >> a.ks_log);
   const unsigned gx = (unsigned)((a.N + per - 1) / per);
-  // with few workgroups the passes over an expert's slots run beside each other
-  const int spp = std::min(16, (NW * kWaveBytes >> a.ks_log) / 528) / (XF == kXBf16 ? 1 : 3);
+  // A pass takes 16 rows, or what two blocks of a slice's staging region hold; with few
+  // workgroups the passes over an expert's slots run beside each other, and while they fit the
+  // chip at once they take up to 4 rows, whose sums are one register a tile (16 bf16 rows, 2048
+  // x 7168: 12.2 us against 17.2, 1003 x 4128: 9.2, 13.8; 4 fp32 rows 11.0, 12.9; but 8 fp32
+  // rows, 1024 workgroups, 16.1, 13.1).
+  constexpr int RPS = XF == kXBf16 ? 1 : 3, SMALL = 4 / RPS;
+  const long wgs = (long)gx * gy, small = (a.S + SMALL - 1) / SMALL;
+  a.spp = wgs * small <= 512 ? SMALL : std::min(16, (NW * kWaveBytes >> a.ks_log) / 528) / RPS;
   const unsigned gz = (unsigned)std::max<long>(
-      1, std::min<long>((a.S + spp - 1) / spp, 512 / ((long)gx * gy)));
+      1, std::min<long>((a.S + a.spp - 1) / a.spp, 512 / wgs));
   hipLaunchKernelGGL((matvec_int4_kernel<NW, XF, SWIGLU, R, GROUP, false>), dim3(gx, gy, gz),
                      dim3(64 * NW), 0, s, a);
   return hipGetLastError();
@@ -544,7 +551,7 @@ hipError_t launch_matvec_int4(const void* x, FewDtype x_dt, int x_div, const uin
                               const float* s7, int group, const int32_t* idx, int S, int G, int N,
                               int K, bool swiglu, void* y, FewDtype y_dt, hipStream_t s) {
   const MatvecArgs a{x, q, s7, idx, S, G, N, K, y,
-                     y_dt == kFewBf16 ? 1 : y_dt == kFewParts ? 2 : 0, 0, 0, nullptr,
+                     y_dt == kFewBf16 ? 1 : y_dt == kFewParts ? 2 : 0, 0, 0, 0, nullptr,
                      (uint32_t)(((1u << 20) + (uint32_t)x_div - 1) / (uint32_t)x_div)};
   return x_dt == kFewBf16    ? launch_matvec_x<kXBf16>(a, group, swiglu, s)
          : x_dt == kFewParts ? launch_matvec_x<kXParts>(a, group, swiglu, s)
@@ -554,7 +561,7 @@ hipError_t launch_matvec_int4(const void* x, FewDtype x_dt, int x_div, const uin
 hipError_t launch_join_int4(const void* h, const uint8_t* q, const float* s7, int group,
                             const int32_t* idx, const float* w, int T, int k, int E, int d, int I,
                             void* y, bool y_bf16, hipStream_t s) {
-  const MatvecArgs a{h, q, s7, idx, T * k, E, d, I, y, y_bf16 ? 1 : 0, 0, k, w, 1u << 20};
+  const MatvecArgs a{h, q, s7, idx, T * k, E, d, I, y, y_bf16 ? 1 : 0, 0, 0, k, w, 1u << 20};
   return group == 32   ? launch_join_g<32>(a, T, s)
          : group == 64 ? launch_join_g<64>(a, T, s)
                        : launch_join_g<128>(a, T, s);
