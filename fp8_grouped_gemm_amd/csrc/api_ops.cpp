@@ -123,13 +123,13 @@ int moe_ffn_int4(const void* x, moe_dtype dt, const uint8_t* w13, const float* s
                                                E, I, d, true, ws, moe::kFewParts, S(stream)),
                        "ffn gate/up launch")))
     return st;
-  // One token's slots name different experts, so nothing is shared and its down products need
-  // not be gathered by expert: they are joined in one kernel, without o and the combine (8 of
-  // 256 experts, 7168 x 2048: 52.5 us the whole FFN, 55.6 with them).  So also where all slots'
-  // weights together are read faster than a launch takes (16 tokens, 2 of 8 experts, 256 x
-  // 512: 12.1, 15.2).  Beyond that each weight once for all its slots is faster: 8 tokens, 1 of
-  // 64 experts, 4096 x 2048: 33.9 us against 42.7.
-  if (T == 1 || (double)slots * d * I <= 16e6)
+  // While a workgroup per token and 16 outputs fits the chip at once, the down products are not
+  // gathered by expert: a token's are joined in one kernel, without o and the combine.  One
+  // token, 8 of 256 experts, 7168 x 2048 (448 workgroups): 52.5 us the whole FFN, 55.6 gathered;
+  // 8 tokens, 6 of 64 experts, 1024 x 512 (512): 17.4, 22.2; 32 tokens, 2 of 8, 256 x 512 (512):
+  // 13.3, 14.8.  Beyond that reading each weight once counts: 16 tokens, 1 of 64, 1024 x 512
+  // (1024): 18.3, 17.5; 8 tokens, 1 of 64, 4096 x 2048 (2048): 42.7, 33.9.
+  if ((long long)((d + 15) / 16) * T <= 512)
     return hip_status(moe::launch_join_int4(ws, w2, s2, group, topk_idx, topk_w, T, k, E, d, I, y,
                                             dt == MOE_BF16, S(stream)),
                       "ffn down launch");
