@@ -19,10 +19,11 @@
 // whose sums are added at the end: the products stay exact.
 //
 // Bound by the reading of the weights.  31 of 256 experts' gate and up rows (2 x 2048 x 7168,
-// 485 MB of codes and scales) take 95 us, 5.1 TB/s, where a bare read of such rows in this
-// order takes 87 and a read front to back 75: every row of a tile is a stream of its own.
-// Slices that interleave, workgroups of 8 waves, of runs of tiles or with all eight waves on
-// one tile measured 96 to 108.
+// 485 MB of codes and scales) take 95 us, 5.1 TB/s.  The loads alone, in this shape, take 87
+// (a bare read of such rows in the same lane order 76); the vector ALU is 44% busy.  Slices
+// that interleave, 8 waves a workgroup, runs of tiles with the ring going on into the next, all
+// eight waves on one tile, rings of 2 or 8 blocks, 12, 20 or 24 waves a CU and x staged before
+// the first weights measured 94 to 108.
 #include <algorithm>
 
 #include "common.hpp"
