@@ -395,7 +395,7 @@ def moe_combine(o: torch.Tensor, row_of_slot: torch.Tensor, topk_w: torch.Tensor
 
 def _want(fn: str, name: str, t: Optional[torch.Tensor], dtype, *shape):
     """Refuse a tensor of another dtype or shape than the call takes (None passes)."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
         raise ValueError(f"{fn}: {name} must be {dtype} {list(shape)}, got {t.dtype} "
                          f"{list(t.shape)}")
 
@@ -508,6 +508,9 @@ def moe_route_bwd_workspace_size(T: int, E: int) -> int:
     return _lib_().moe_route_bwd_workspace_size(T, E)
 
 
+_BALANCE_KINDS = {"switch": _lib.MOE_BALANCE_SWITCH, "square": _lib.MOE_BALANCE_SQUARE}
+
+
 def _router_args(fn, logits, topk_idx, bias, mask, offsets):
     T, E = logits.shape
     B = 1 if offsets is None else offsets.numel() - 1
@@ -516,10 +519,9 @@ def _router_args(fn, logits, topk_idx, bias, mask, offsets):
     _want(fn, "topk_idx", topk_idx, torch.int32, T, k)
     _want(fn, "bias", bias, torch.float32, E)
     _want(fn, "offsets", offsets, torch.int32, B + 1)
-    if mask is not None and mask.dtype == torch.bool:
-        mask = mask.view(torch.uint8)
-    _want(fn, "mask", mask, torch.uint8, T)
-    return T, E, k, B, mask
+    if mask is not None:                                # a bool is a byte
+        _want(fn, "mask", mask, torch.bool if mask.dtype == torch.bool else torch.uint8, T)
+    return T, E, k, B
 
 
 @_on_tensor_device
@@ -532,10 +534,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
     is nonzero.  kind "switch": coef E sum f_e P_e; "square": coef sum (P_e - 1/E)^2.
     Returns (loss [], counts [B, E], probs [B, E], grad [B, E]); grad goes to moe_route_bwd."""
     fn = "moe_balance_loss"
-    kinds = {"switch": _lib.MOE_BALANCE_SWITCH, "square": _lib.MOE_BALANCE_SQUARE}
-    if kind not in kinds:
-        raise ValueError(f"{fn}: kind must be one of {sorted(kinds)}, got {kind!r}")
-    T, E, k, B, mask = _router_args(fn, logits, topk_idx, bias, mask, offsets)
+    if kind not in _BALANCE_KINDS:
+        raise ValueError(f"{fn}: kind must be one of {sorted(_BALANCE_KINDS)}, got {kind!r}")
+    T, E, k, B = _router_args(fn, logits, topk_idx, bias, mask, offsets)
     dev = logits.device
     counts = torch.empty((B, E), dtype=torch.int32, device=dev)
     probs = torch.empty((B, E), dtype=torch.float32, device=dev)
@@ -544,9 +545,10 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
     if workspace is None:
         workspace = torch.empty(moe_balance_workspace_size(T, E, B), dtype=torch.uint8, device=dev)
     _lib.check(_lib_().moe_balance_loss(_ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(mask),
-                                        _ptr(offsets), T, E, k, B, kinds[kind], coef,
-                                        _ptr(counts), _ptr(probs), _ptr(grad), _ptr(loss),
-                                        _ptr(workspace), _nbytes(workspace), _stream(dev)), fn)
+                                        _ptr(offsets), T, E, k, B, _BALANCE_KINDS[kind], coef,
+                                        counts.data_ptr(), probs.data_ptr(), grad.data_ptr(),
+                                        loss.data_ptr(), _ptr(workspace), _nbytes(workspace),
+                                        _stream(dev)), fn)
     return loss, counts, probs, grad
 
 
@@ -562,7 +564,7 @@ def moe_route_bwd(logits: torch.Tensor, topk_idx: Optional[torch.Tensor] = None,
     (balance_grad [B, E], its upstream gradient dloss, one fp32 on the GPU, 1 if None) with
     respect to the logits.  Returns dlogits [T, E], or (dlogits, dbias [E]) with need_dbias."""
     fn = "moe_route_bwd"
-    T, E, k, B, mask = _router_args(fn, logits, topk_idx, bias, mask, offsets)
+    T, E, k, B = _router_args(fn, logits, topk_idx, bias, mask, offsets)
     dev = logits.device
     _want(fn, "dtopk_w", dtopk_w, torch.float32, T, k)
     _want(fn, "balance_grad", balance_grad, torch.float32, B, E)
