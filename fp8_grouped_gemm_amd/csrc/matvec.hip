@@ -37,6 +37,9 @@ constexpr int kMaxSlots = 1024;
 // LDS for staged x, per wave: with a slice of K per wave two blocks of 13 rows fit, and the
 // workgroups that the registers allow (16 waves a CU) fit the CU's LDS.
 constexpr int kWaveBytes = 7168;
+// Row tiles of a pass where experts have many slots, and the staged x of their workgroups:
+// with K in 2 slices two blocks of 48 rows.
+constexpr int kManyTiles = 3, kManyBytes = 14336;
 constexpr int kRing = 4;                // blocks of codes a wave has in flight (few rows)
 
 __device__ __forceinline__ void store_out(void* y, size_t i, float v, bool bf16) {
@@ -160,16 +163,17 @@ __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + expf(-z)
 
 // JOIN: the outputs of a token are the sums over its k slots, times the slots' weights, and
 // each slot's product is a wave's (or several waves', over K).
-template <int NW, int XF, bool SWIGLU, int R, int GROUP, bool JOIN>
-__global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
+// MT > 1: passes of 16 MT rows, for which a code is expanded once.
+template <int NW, int XF, bool SWIGLU, int R, int GROUP, bool JOIN, int MT>
+__global__ __launch_bounds__(64 * NW, MT > 1 ? 2 : 4) void matvec_int4_kernel(MatvecArgs a) {
   static_assert(!SWIGLU || R == 2, "SwiGLU: one gate and one up tile");
   constexpr int NT = NW * 64;
   constexpr int RPS = XF == kXBf16 ? 1 : 3;        // left-operand rows per slot
   constexpr int GP = 128 / GROUP;                  // groups per block
   constexpr int NO = SWIGLU ? 16 : 16 * R;         // outputs per wave
   constexpr int SCH = 16 / GP, SST = 17;           // blocks of staged scales, floats per row
-  constexpr int XBYTES = NW * kWaveBytes;
-  static_assert(NW * R * 4 * 64 * 4 <= XBYTES, "the waves' sums reuse the staging region");
+  constexpr int XBYTES = NW * (MT > 1 ? kManyBytes : kWaveBytes);
+  static_assert(NW * R * MT * 4 * 64 * 4 <= XBYTES, "the waves' sums reuse the staging region");
   __shared__ uint16_t slots[kMaxSlots];            // slots of the expert
   // A staged row ends 16 bytes off a multiple of the banks, so that the rows of one read fall
   // into different ones.
@@ -294,9 +298,11 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
     auto slot_at = [&](int i) { return JOIN ? own : a.idx ? (int)slots[s0 + i] : s0 + i; };
     // slot / x_div by a multiplication: exact for slots below 1024
     auto x_row = [&](int slot) { return (size_t)(((uint32_t)slot * a.inv_div) >> 20); };
-    v4f acc[R];
+    v4f acc[R][MT];
 #pragma unroll
-    for (int t = 0; t < R; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[t][m] = v4f{0.f, 0.f, 0.f, 0.f};
 
     auto run = [&](auto MRC) {
       constexpr int MR = decltype(MRC)::value;
@@ -307,9 +313,12 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
       const int ch = min((room / nr - 16) / 256, max(nb_max + U - 1, U)) / U * U;
       const int xst = ch * 256 + 16;
       uint8_t* xs = xs_mem + (JOIN ? wid : ks) * room;
-      // left-operand row i sits at matrix row 4 (i % 4) + i / 4, so that up to four rows
-      // leave each lane one sum; rows past nr repeat the last one
-      const uint8_t* xlane = xs + min((l16 >> 2) + 4 * (l16 & 3), nr - 1) * xst;
+      // left-operand row i of a tile sits at matrix row 4 (i % 4) + i / 4, so that up to four
+      // rows leave each lane one sum; rows past nr repeat the last one
+      const uint8_t* xlane[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        xlane[m] = xs + min(16 * m + (l16 >> 2) + 4 * (l16 & 3), nr - 1) * xst;
 
       // x rows of the blocks [c0, c0 + n) of this slice by the slice's waves, zeros past K
       // and in the blocks that fill up the ring's last turn; all loads of a turn are issued
@@ -363,10 +372,40 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
 
       // block `at` of the chunk, block `sat` of the staged scales
       auto compute = [&](v4i (&w)[R], int at, int sat) {
+        if constexpr (MT > 1) {
+#pragma unroll
+          for (int t = 0; t < R; ++t) {
+            regroup<GROUP>(w[t]);
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+              v4f p[MT];
+#pragma unroll
+              for (int m = 0; m < MT; ++m) p[m] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = g * (4 / GP); i < (g + 1) * (4 / GP); ++i) {
+                const v8bf lo = fp4_codes((uint32_t)w[t][i] & 0xBBBBBBBBu);
+                const v8bf hi = fp4_codes((uint32_t)w[t][i] & 0xCCCCCCCCu);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                  const v8bf xa = *reinterpret_cast<const v8bf*>(
+                      xlane[m] + at * 256 + 16 * word_of<GROUP>(h, i));
+                  p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, lo, p[m], 0, 0, 0);
+                  p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, hi, p[m], 0, 0, 0);
+                }
+              }
+              const float s = sc[(16 * t + l16) * SST + sat * GP + g];
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < MR; ++r) acc[t][m][r] = fmaf(s, p[m][r], acc[t][m][r]);
+            }
+          }
+          return;
+        }
         v8bf xa[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          xa[i] = *reinterpret_cast<const v8bf*>(xlane + at * 256 + 16 * word_of<GROUP>(h, i));
+          xa[i] = *reinterpret_cast<const v8bf*>(xlane[0] + at * 256 + 16 * word_of<GROUP>(h, i));
 #pragma unroll
         for (int t = 0; t < R; ++t) {
           regroup<GROUP>(w[t]);
@@ -378,7 +417,7 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
               p = mul_codes(xa[i], (uint32_t)w[t][i], p);
             const float s = sc[(16 * t + l16) * SST + sat * GP + g];
 #pragma unroll
-            for (int r = 0; r < MR; ++r) acc[t][r] = fmaf(s, p[r], acc[t][r]);
+            for (int r = 0; r < MR; ++r) acc[t][0][r] = fmaf(s, p[r], acc[t][0][r]);
           }
         }
       };
@@ -417,18 +456,20 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
       }
       if constexpr (JOIN) return;
       __syncthreads();
-      float* red = reinterpret_cast<float*>(xs_mem) + wid * (R * 4 * 64);
+      float* red = reinterpret_cast<float*>(xs_mem) + wid * (R * MT * 4 * 64);
 #pragma unroll
       for (int t = 0; t < R; ++t)
 #pragma unroll
-        for (int r = 0; r < MR; ++r) red[(t * 4 + r) * 64 + lane] = acc[t][r];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int r = 0; r < MR; ++r) red[((t * MT + m) * 4 + r) * 64 + lane] = acc[t][m][r];
     };
     if constexpr (JOIN) {
       run(std::integral_constant<int, 1>{});
 #pragma unroll
-      for (int t = 0; t < R; ++t) tot[t] = valid ? fmaf(a.wgt[own], acc[t][0], tot[t]) : tot[t];
+      for (int t = 0; t < R; ++t) tot[t] = valid ? fmaf(a.wgt[own], acc[t][0][0], tot[t]) : tot[t];
       continue;
-    } else if (nr <= 4) {
+    } else if (MT == 1 && nr <= 4) {
       run(std::integral_constant<int, 1>{});
     } else {
       run(std::integral_constant<int, 4>{});
@@ -446,9 +487,10 @@ __global__ __launch_bounds__(64 * NW, 4) void matvec_int4_kernel(MatvecArgs a) {
         const int t = SWIGLU ? t2 : c >> 4;
 #pragma unroll
         for (int p = RPS - 1; p >= 0; --p) {
-          const int i = sl * RPS + p, at = (t * 4 + (i >> 2)) * 64 + 16 * (i & 3) + (c & 15);
+          const int i = sl * RPS + p;                  // (tile i / 16, register i / 4 % 4)
+          const int at = (t * MT * 4 + (i >> 2)) * 64 + 16 * (i & 3) + (c & 15);
           float z = 0.f;
-          for (int w = 0; w < KS; ++w) z += red[(w0 + w) * (R * 4 * 64) + at];
+          for (int w = 0; w < KS; ++w) z += red[(w0 + w) * (R * MT * 4 * 64) + at];
           v[t2] += z;
         }
         v[t2] *= kCodeUnit;
@@ -507,14 +549,40 @@ hipError_t launch_matvec_r(MatvecArgs a, unsigned gy, hipStream_t s) {
   a.spp = wgs * small <= 512 ? SMALL : std::min(16, (NW * kWaveBytes >> a.ks_log) / 528) / RPS;
   const unsigned gz = (unsigned)std::max<long>(
       1, std::min<long>((a.S + a.spp - 1) / a.spp, 512 / wgs));
-  hipLaunchKernelGGL((matvec_int4_kernel<NW, XF, SWIGLU, R, GROUP, false>), dim3(gx, gy, gz),
+  hipLaunchKernelGGL((matvec_int4_kernel<NW, XF, SWIGLU, R, GROUP, false, 1>), dim3(gx, gy, gz),
                      dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+
+// Experts with many slots: 48 rows a pass (16 fp32 rows).
+template <int XF, bool SWIGLU, int GROUP>
+hipError_t launch_matvec_many(MatvecArgs a, unsigned gy, hipStream_t s) {
+  constexpr int NW = 4, RPS = XF == kXBf16 ? 1 : 3;
+  const int per = (SWIGLU ? 16 : 32) * NW;
+  a.ks_log = (long)((a.N + per - 1) / per) * gy >= 512 ? 0 : 1;
+  const unsigned gx = (unsigned)((a.N + (per >> a.ks_log) - 1) / (per >> a.ks_log));
+  a.spp = 16 * kManyTiles / RPS;
+  const unsigned gz = (unsigned)std::max<long>(
+      1, std::min<long>((a.S + a.spp - 1) / a.spp, 512 / ((long)gx * gy)));
+  hipLaunchKernelGGL((matvec_int4_kernel<NW, XF, SWIGLU, 2, GROUP, false, kManyTiles>),
+                     dim3(gx, gy, gz), dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 
 template <int XF, int GROUP>
 hipError_t launch_matvec_g(MatvecArgs a, bool swiglu, hipStream_t s) {
   const unsigned gy = a.idx ? (unsigned)(a.S <= a.G ? a.S : a.G) : 1u;
+  // Where experts have more than 16 rows of x on average, 48 rows a pass save reading and
+  // expanding the codes again, if the products are large enough to fill the chip with fewer
+  // workgroups (by weight rows times passes: 128 bf16 rows of 4096 x 2048, 33k, 20 us against 29,
+  // 64 of them, 16k, 20 against 16; 64 fp32 rows of 2048 x 7168, 25k, 43 against 52, 32 of them, 12k, 43
+  // against 27; 24 tokens' FFN with all 4 experts, 7168 x 2048, in fp32 96 against 178).
+  constexpr int RPS = XF == kXBf16 ? 1 : 3;
+  const long mean = ((long)a.S * RPS + (a.idx ? a.G : 1) - 1) / (a.idx ? a.G : 1);
+  if (mean > 16 && (mean + 15) / 16 * gy * a.N * (swiglu ? 2 : 1) >= 20000) {
+    if (!swiglu) return launch_matvec_many<XF, false, GROUP>(a, gy, s);
+    if constexpr (XF != kXParts) return launch_matvec_many<XF, true, GROUP>(a, gy, s);
+  }
   const long tiles = ((long)a.N + (swiglu ? 15 : 31)) / (swiglu ? 16 : 32) * gy;
   // Enough waves for the chip, in slices long enough to stream: K whole for short rows of
   // which there are many (101 experts' down products, 7168 x 2048 each: 165 us, in 2 slices
@@ -537,7 +605,7 @@ hipError_t launch_join_g(MatvecArgs a, int T, hipStream_t s) {
   constexpr int NW = 8;
   a.ks_log = a.k > 4 ? 0 : a.k > 2 ? 1 : a.k > 1 ? 2 : 3;
   const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)T), block(64 * NW);
-  hipLaunchKernelGGL((matvec_int4_kernel<NW, kXParts, false, 1, GROUP, true>), grid, block, 0, s, a);
+  hipLaunchKernelGGL((matvec_int4_kernel<NW, kXParts, false, 1, GROUP, true, 1>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

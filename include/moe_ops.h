@@ -50,8 +50,8 @@ int moe_quant_weight_int4_group(const float *w, int G, int N, int K, int group, 
  *   positive multiple of group, K <= 2^24; 1 <= N <= 2^24; 1 <= G <= 65536;
  *   0 <= S <= MOE_FEW_SLOTS_MAX; x_div >= 1 (1 without idx).  x and q 16-byte aligned.  y
  *   must not overlap an input (not checked).
- * Slots may name the same expert (its weights are then read once for up to 16 rows of x,
- * an fp32 row counting as three) and the same row. */
+ * Slots may name the same expert (its weights are then read once for up to 16 or 48 rows of
+ * x, an fp32 row counting as three) and the same row. */
 int moe_matvec_int4(const void *x, moe_dtype x_dt, int x_div, const uint8_t *q, const float *s7,
                     int group, const int32_t *idx, int S, int G, int N, int K, int epilogue,
                     void *y, moe_dtype y_dt, void *stream);

@@ -143,6 +143,32 @@ def test_matvec_routed(T, k, G, N, K, group, x_dt, epi):
     assert np.all(to_np(y)[out] == 0)
 
 
+@pytest.mark.parametrize("T, k, G, N, K, group", [
+    # passes of 48 rows: all of a matrix, and experts with uneven numbers of slots
+    (200, 0, 1, 2001, 160, 32), (64, 0, 1, 8200, 192, 64), (130, 0, 1, 2600, 1152, 128),
+    (64, 4, 2, 2500, 96, 32), (170, 6, 5, 1300, 320, 64), (49, 1, 1, 10300, 128, 128),
+])
+@pytest.mark.parametrize("x_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("epi", ["plain", "swiglu"])
+def test_matvec_many_slots_an_expert(T, k, G, N, K, group, x_dt, epi):
+    note(f"matvec many T={T} k={k} G={G} N={N} K={K} group={group} {x_dt} {epi}")
+    r = gen(T + N)
+    nb = 2 * N if epi == "swiglu" else N
+    q, s = weights(r, G, nb, K, group)
+    x, x64 = rows(r, T, K, DT[x_dt])
+    idx = None
+    if k:
+        # the first expert gets most slots; some get none
+        idx = np.minimum(r.integers(-1, 2 * G, T * k), G - 1).astype(np.int32)
+    v, absum = OP.matvec_int4(x64, OP.int4_weight(q, s), idx, max(k, 1))
+    err = sum_error(absum, K, group)
+    if epi == "swiglu":
+        v, err = swiglu(v, err)
+    y = M.moe_matvec_int4(x, t_(q), t_(s), None if idx is None else t_(idx), x_div=max(k, 1),
+                          swiglu=epi == "swiglu", out_dtype=torch.float32)
+    check(y, v, err)
+
+
 def test_matvec_1024_slots_of_one_expert():
     note("matvec 1024 slots")
     r = gen(9)
@@ -251,6 +277,8 @@ def test_ffn(T, k, E, d, I, group, dt):
     (1, 1, 3, 1056, 2080, 32), (1, 2, 9, 320, 1984, 64), (1, 3, 9, 128, 384, 128),
     (1, 4, 9, 224, 4128, 32), (1, 5, 9, 64, 64, 64), (1, 9, 12, 192, 896, 64),
     (1, 16, 16, 160, 32, 32), (1, 17, 20, 384, 1152, 128),
+    # many slots an expert
+    (96, 4, 3, 2080, 672, 32), (64, 4, 4, 1280, 1920, 64), (128, 8, 8, 1024, 640, 128),
     # many: gathered by expert
     (64, 8, 4, 256, 256, 64), (200, 2, 3, 224, 416, 32), (24, 1, 6, 1152, 640, 128),
     (2, 3, 5, 2080, 2080, 32),
@@ -622,7 +650,7 @@ def test_gathered_calls_on_streams_and_captured():
     among eager calls."""
     note("gathered, streams and graph")
     r = gen(72)
-    T, k, E, d, I = 64, 8, 4, 256, 256
+    T, k, E, d, I = 64, 8, 4, 1024, 256
     w13, s13 = (t_(v) for v in weights(r, E, 2 * I, d, 64))
     w2, s2 = (t_(v) for v in weights(r, E, d, I, 64))
     x, _ = rows(r, T, d, torch.bfloat16)
