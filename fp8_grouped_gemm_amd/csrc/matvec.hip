@@ -322,12 +322,12 @@ __global__ __launch_bounds__(64 * NW, MT > 1 ? 2 : 4) void matvec_int4_kernel(Ma
 
       // x rows of the blocks [c0, c0 + n) of this slice by the slice's waves, zeros past K
       // and in the blocks that fill up the ring's last turn; all loads of a turn are issued
-      // before the first is waited for
+      // before the first is waited for (48 rows: a slice's whole chunk by two waves)
       auto stage = [&](int c0, int n) {
         const int nb = (n + U - 1) / U * U;
         const int nu = (XF == kXF32 ? ns : nr) * nb;   // 16-lane units: a row's block
         const float inv = 1.0f / (float)nb;
-        constexpr int XV = XF == kXF32 ? 2 : 1, TURN = 4 / XV;
+        constexpr int XV = XF == kXF32 ? 2 : 1, TURN = (MT > 1 ? 12 : 4) / XV;
         for (int u0 = stage_i * 4; u0 < nu; u0 += stage_n * 4 * TURN) {
           v4i v[TURN][XV];
           int dst[TURN];
@@ -383,15 +383,19 @@ __global__ __launch_bounds__(64 * NW, MT > 1 ? 2 : 4) void matvec_int4_kernel(Ma
               for (int m = 0; m < MT; ++m) p[m] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int i = g * (4 / GP); i < (g + 1) * (4 / GP); ++i) {
+                v8bf xa[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                  xa[m] = *reinterpret_cast<const v8bf*>(xlane[m] + at * 256 +
+                                                         16 * word_of<GROUP>(h, i));
                 const v8bf lo = fp4_codes((uint32_t)w[t][i] & 0xBBBBBBBBu);
                 const v8bf hi = fp4_codes((uint32_t)w[t][i] & 0xCCCCCCCCu);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  const v8bf xa = *reinterpret_cast<const v8bf*>(
-                      xlane[m] + at * 256 + 16 * word_of<GROUP>(h, i));
-                  p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, lo, p[m], 0, 0, 0);
-                  p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, hi, p[m], 0, 0, 0);
-                }
+                for (int m = 0; m < MT; ++m)
+                  p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[m], lo, p[m], 0, 0, 0);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                  p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[m], hi, p[m], 0, 0, 0);
               }
               const float s = sc[(16 * t + l16) * SST + sat * GP + g];
 #pragma unroll
@@ -574,9 +578,10 @@ hipError_t launch_matvec_g(MatvecArgs a, bool swiglu, hipStream_t s) {
   const unsigned gy = a.idx ? (unsigned)(a.S <= a.G ? a.S : a.G) : 1u;
   // Where experts have more than 16 rows of x on average, 48 rows a pass save reading and
   // expanding the codes again, if the products are large enough to fill the chip with fewer
-  // workgroups (by weight rows times passes: 128 bf16 rows of 4096 x 2048, 33k, 20 us against 29,
-  // 64 of them, 16k, 20 against 16; 64 fp32 rows of 2048 x 7168, 25k, 43 against 52, 32 of them, 12k, 43
-  // against 27; 24 tokens' FFN with all 4 experts, 7168 x 2048, in fp32 96 against 178).
+  // workgroups (by weight rows times passes: 128 bf16 rows of 4096 x 2048, 33k, 19 us against
+  // 29, 64 of them, 16k, 20 against 16; 64 fp32 rows of 2048 x 7168, 25k, 43 against 52, 32 of
+  // them, 12k, 43 against 27; 24 tokens' FFN with all 4 experts, 7168 x 2048, in fp32 92 against
+  // 178).
   constexpr int RPS = XF == kXBf16 ? 1 : 3;
   const long mean = ((long)a.S * RPS + (a.idx ? a.G : 1) - 1) / (a.idx ? a.G : 1);
   if (mean > 16 && (mean + 15) / 16 * gy * a.N * (swiglu ? 2 : 1) >= 20000) {
